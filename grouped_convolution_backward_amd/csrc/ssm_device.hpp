@@ -254,16 +254,13 @@ __device__ __forceinline__ Piece find_piece(const Pieces& pc, int id) {
             if (k < 64) break;
         }
         r.n = __builtin_amdgcn_readfirstlane(max(found - 1, 0));
-        const int s = min(max(pc.seq_start[r.n], 0), pc.T);
-        const int e = min(max(pc.seq_start[r.n + 1], s), min(pc.T, s + pc.L));
-        r.row0 = __builtin_amdgcn_readfirstlane(s);
-        r.len = __builtin_amdgcn_readfirstlane(e - s);
+        const SeqRows q = packed_rows(pc.seq_start[r.n], pc.seq_start[r.n + 1], pc.T, pc.L);
+        r.row0 = __builtin_amdgcn_readfirstlane(q.row0);
+        r.len = __builtin_amdgcn_readfirstlane(q.len);
         r.j = id - (r.row0 / pc.rows + r.n);
     }
-    const bool some = r.j >= 0 && r.j <= r.len / pc.rows;   // ids between two sequences name no piece
-    r.t0 = some ? r.j * pc.rows : r.len;
-    r.rows = min(r.len - r.t0, pc.rows);
-    r.last = some && (r.j == 0 ? r.len <= pc.rows : (r.rows > 0 && r.len - r.t0 <= pc.rows));
+    const PieceRows p = piece_rows(r.j, r.len, pc.rows);    // ids between two sequences name no piece
+    r.t0 = p.t0, r.rows = p.rows, r.last = p.last;
     return r;
 }
 

@@ -24,6 +24,27 @@ struct Pieces {
     int32_t count;              // piece ids in all
 };
 
+// The rows of a packed sequence from two neighbouring values of seq_start,
+// whatever they are: 0 <= row0 <= row0 + len <= T and len <= L. No sum of two
+// of the numbers is formed, since T and L go up to 2^30 each. Host and device.
+struct SeqRows { int32_t row0, len; };
+constexpr SeqRows packed_rows(int32_t from, int32_t to, int32_t T, int32_t L) {
+    const int32_t s = from < 0 ? 0 : from > T ? T : from;
+    const int32_t e = to < s ? s : to > T ? T : to;
+    return {s, e - s < L ? e - s : L};
+}
+
+// Where piece j of a sequence of len rows lies in it, for any j: its first row
+// and its rows (<= 0: none), and whether the sequence ends with it. A piece
+// that the sequence does not have starts, without rows, at the sequence's end.
+struct PieceRows { int32_t t0, rows; bool last; };
+constexpr PieceRows piece_rows(int32_t j, int32_t len, int32_t rows) {
+    const bool some = j >= 0 && j <= len / rows;
+    const int32_t t0 = some ? j * rows : len;
+    const int32_t left = len - t0;
+    return {t0, left < rows ? left : rows, some && (j == 0 ? len <= rows : left > 0 && left <= rows)};
+}
+
 struct CconvArgs {
     const void *x, *w, *bias, *init, *dy, *dfinal;
     void *y, *final_state, *dx, *dinit;
