@@ -46,13 +46,13 @@ struct Rows {
         nv = nv_;
         have_init = a.init;
     }
-    __device__ __forceinline__ uint32_t at(int t, int stride) const { return (uint32_t)((t - base) * stride + c); }
+    __device__ __forceinline__ uint32_t at(int t, int stride) const { return row_offset(t, base, stride, c); }
     __device__ __forceinline__ void row(Pack<T, E>& v, int t) const { v.load(x, at(t, sx), VEC, t < len ? nv : 0); }
     // row t of a window: the sequence's for t >= 0, its initial state's for -(W-1) <= t < 0
     __device__ __forceinline__ void window(Pack<T, E>& v, int t) const {
         Pack<T, E> s;
         v.load(x, at(t, sx), VEC, t >= 0 && t < len ? nv : 0);
-        s.load(init, (uint32_t)((t + W - 1) * C + c), VEC, have_init && t < 0 ? nv : 0);
+        s.load(init, row_offset(t, 1 - W, C, c), VEC, have_init && t < 0 ? nv : 0);
 #pragma unroll
         for (int i = 0; i < Pack<T, E>::kWords; ++i) v.w[i] |= s.w[i];     // one of them is zeros
     }

@@ -45,6 +45,13 @@ constexpr PieceRows piece_rows(int32_t j, int32_t len, int32_t rows) {
     return {t0, left < rows ? left : rows, some && (j == 0 ? len <= rows : left > 0 && left <= rows)};
 }
 
+// The byte offset, from row `base` of a tensor on, of place `at` in row t. For
+// rows that are not accessed (their offsets go out of range afterwards) it is
+// any number, so it is formed modulo 2^32. Host and device.
+constexpr uint32_t row_offset(int32_t t, int32_t base, int32_t row_bytes, int32_t at) {
+    return ((uint32_t)t - (uint32_t)base) * (uint32_t)row_bytes + (uint32_t)at;
+}
+
 struct CconvArgs {
     const void *x, *w, *bias, *init, *dy, *dfinal;
     void *y, *final_state, *dx, *dinit;

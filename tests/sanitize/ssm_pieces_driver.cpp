@@ -1,7 +1,9 @@
 // The device's arithmetic on seq_start values (packed_rows, piece_rows) over
 // valid and invalid ones, up to the largest problems a plan accepts. Built with
 // UndefinedBehaviorSanitizer, which ends the program at the first overflow;
-// the sums here are 64-bit. Prints the number of combinations looked at.
+// the sums here are 64-bit. Likewise the offsets of rows in a piece of the
+// convolution (row_offset), which its kernels also form for rows far outside
+// it. Prints the number of combinations looked at.
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -45,6 +47,15 @@ int main() {
                         }
                     }
                 }
+    for (int32_t row_bytes : {2, 4, 1 << 12, 1 << 21, 1 << 22})      // strides up to 2^20 elements of 4 bytes
+        for (int32_t base : {-7, 0, 5, big - 300, big - 1})
+            for (int64_t d : {-7, -1, 0, 1, 255, 263, 300, big - 300, big}) {
+                const int32_t t = (int32_t)(base + d < big + 300 ? base + d : big);
+                const uint32_t got = row_offset(t, base, row_bytes, 40);
+                const int64_t want = ((int64_t)t - base) * row_bytes + 40;
+                expect(got == (uint32_t)want, "another offset", t, base, row_bytes, 40, 0, 0);
+                if (d >= 0 && d <= 263) expect((int64_t)got == want && want < (1LL << 31), "offset of a near row", t, base, row_bytes, 40, 0, 0);
+            }
     std::printf("%lld\n", g_seen);
     return 0;
 }

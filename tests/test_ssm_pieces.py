@@ -1,7 +1,7 @@
 """The arithmetic by which the kernels of the causal convolution and the
-selective scan find their rows from seq_start, built from the kernels' own
-header by g++ with UndefinedBehaviorSanitizer and run over valid and invalid
-values up to the largest problems that a plan accepts."""
+selective scan find their rows from seq_start, and their places in them, built
+from the kernels' own header by g++ with UndefinedBehaviorSanitizer and run
+over valid and invalid values up to the largest problems that a plan accepts."""
 
 import os
 import shutil
