@@ -476,18 +476,40 @@ def wgrad_scan_step_run(plan: ScanPlan, *args, **kw) -> None:
     plan.run_step(*args, **kw)
 
 
-def causal_conv(problem: dict, x, w, bias=None, **kw):
-    """Convenience: plan, allocate y with torch, run."""
+def _on_stream(x, stream, call):
+    """call() with `stream` (as the plans take it) as the current one, so that what it allocates belongs to the stream that
+    the kernels run on; its result may then be used on the caller's current stream too."""
     import torch
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    CausalConvPlan(problem).run(x, w, y, bias=bias, **kw)
+    if stream is None:
+        return call()
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    here = torch.cuda.current_stream(x.device)
+    there = torch.cuda.ExternalStream(handle, x.device) if handle else torch.cuda.default_stream(x.device)
+    with torch.cuda.stream(there):
+        y = call()
+    y.record_stream(here)
     return y
 
 
-def selective_scan(problem: dict, x, delta, A, B, C, **kw):
-    """Convenience: plan, allocate y (and the workspace) with torch, run."""
+def causal_conv(problem: dict, x, w, bias=None, stream=None, **kw):
+    """Convenience: plan, allocate y with torch, run. On another stream than the current one the caller orders that stream
+    after its inputs, and the use of y after it."""
     import torch
-    plan = ScanPlan(problem)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    plan.run(x, delta, A, B, C, y, ws=plan.new_workspace(x.device) if plan.workspace_bytes else None, **kw)
-    return y
+
+    def call():
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        CausalConvPlan(problem).run(x, w, y, bias=bias, **kw)
+        return y
+    return _on_stream(x, stream, call)
+
+
+def selective_scan(problem: dict, x, delta, A, B, C, stream=None, **kw):
+    """Convenience: plan, allocate y (and the workspace) with torch, run. Streams as with causal_conv."""
+    import torch
+
+    def call():
+        plan = ScanPlan(problem)
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        plan.run(x, delta, A, B, C, y, ws=plan.new_workspace(x.device) if plan.workspace_bytes else None, **kw)
+        return y
+    return _on_stream(x, stream, call)
