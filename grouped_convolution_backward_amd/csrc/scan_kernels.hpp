@@ -610,6 +610,10 @@ __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(co
 #pragma unroll
             for (int i = 0; i < NS; ++i) e[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[i] * sd), e[i], s[i]);
         }
+        // lanes past the block's last channel read another channel's records: their e enters the sums over channels, where 0
+        // times it is not 0 if it is infinite
+#pragma unroll
+        for (int i = 0; i < NS; ++i) e[i] = ok ? e[i] : 0.f;
     }
     const CS cs(lane);
     // where this lane's first sum goes in a partial row

@@ -1,0 +1,55 @@
+"""Infinite and NaN operands of the selective scan and the causal convolution
+on the GPU: what the formulas keep finite stays finite, and right, whatever
+stands in other channels, groups, sequences and padding."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+gcb = pytest.importorskip("grouped_convolution_backward_amd")
+
+import ssm_reference as ref  # noqa: E402
+from test_gpu_ssm import _ref_scan, _run_scan, _scan_case  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+
+def same(name, a, b):
+    assert torch.equal(a, b), f"{name}: {int((a != b).sum())} of {a.numel()} values differ"
+
+
+def _same_where_finite(got, want, scale, dtype, L, C, T):
+    """Outputs are finite exactly where the 64-bit form is, and there within its bound."""
+    terms = {"dB": C, "dC": C, "dA": T, "dD": T, "ddelta_bias": T}
+    for k, v in got.items():
+        kind = "fp32" if k in ("final_state", "dinit_state", "dA", "dD", "ddelta_bias") else dtype
+        g, w, s = v.double().cpu().reshape(-1), want[k].reshape(-1), scale[k].reshape(-1)
+        fine = torch.isfinite(w)
+        assert torch.equal(torch.isfinite(g), fine), f"{k}: {int((torch.isfinite(g) != fine).sum())} of {g.numel()} values"
+        ref.assert_close(k, g[fine], w[fine], s[fine], kind, 4 * L + 64 + terms.get(k, 128))
+
+
+@pytest.mark.parametrize("value", [INF, NAN])
+@pytest.mark.parametrize("dtype,C,S,G,segments", [("bf16", 40, 16, 2, 3), ("fp32", 262, 8, 2, 3), ("fp32", 36, 40, 3, 2),
+                                                  ("bf16", 70, 16, 2, 0)])
+def test_a_gradient_that_is_not_finite_stays_in_its_group(dtype, C, S, G, segments, value):
+    """dy of channel 0 in the last segment: its group's dB and dC, its own gradients in rows before, and nothing else. Channels
+    past the end of another group's last block must not carry it there."""
+    c, p, starts, T = _scan_case(dtype, C, S, G, 1, 150, None, True, True)
+    plan = gcb.ScanPlan(p, segments=segments, segments_backward=segments)
+    print(f"[gpu] scan {p} {plan.info}", flush=True)
+    clean = _run_scan(plan, c, starts, T)
+    c["dy"][T - 2, 0] = value
+    got = _run_scan(plan, c, starts, T)
+    for k in ("dB", "dC"):
+        same(k, got[k][:, 1:], clean[k][:, 1:])
+        assert not bool(torch.isfinite(got[k][T - 2, 0]).any()), k
+    for k in ("dx", "ddelta", "dz", "dinit_state"):
+        same(k, got[k][:, 1:], clean[k][:, 1:])
+    for k in ("dA", "dD", "ddelta_bias"):
+        same(k, got[k][1:], clean[k][1:])
+    for k in ("y", "final_state"):
+        same(k, got[k], clean[k])
+    want, scale = _ref_scan(c, starts)
+    _same_where_finite(got, want, scale, dtype, 150, C, T)
