@@ -112,11 +112,13 @@ __device__ __forceinline__ void write_pairs(f32x2* row, int ec, const float (&a)
 }
 
 // A lane's states' rates, times log2(e) for the hardware's 2^x. Padding
-// states have rate 0 and B = C = 0: they stay 0 and add nothing.
+// states have B = C = 0: they stay 0 and add nothing. Their rate is negative,
+// so that an infinite step is a decay of 0 to them (with a rate of 0 it would
+// be NaN, which 0 times it is too).
 template <int NS>
 __device__ __forceinline__ void load_rates(const ScanArgs& a, int c, bool ok, int s0, float (&A2)[NS]) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) A2[i] = ok && s0 + i < a.S ? a.A[(int64_t)c * a.S + s0 + i] * kLog2e : 0.f;
+    for (int i = 0; i < NS; ++i) A2[i] = ok && s0 + i < a.S ? a.A[(int64_t)c * a.S + s0 + i] * kLog2e : -1.f;
 }
 template <int NS>
 __device__ __forceinline__ void load_state(const ScanArgs& a, const float* p, int n, int c, bool ok, int s0, float (&h)[NS]) {
@@ -315,7 +317,7 @@ __global__ __launch_bounds__(256) void fwd_kernel(const ScanArgs a) {
             float dv[E], u[E];
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                // rows past the end: decay 1, nothing added (channels past the end have rate 0 and x 0)
+                // rows past the end: decay 1, nothing added (channels past the end have x 0)
                 dv[i] = live ? d[k * E + i] : 0.f;
                 u[i] = dv[i] * x[k].get(i);
             }
@@ -685,7 +687,7 @@ __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(co
             const bool live = t0 + t < rows;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                // rows past the end: decay 1, nothing added (channels past the end have rate 0, x and dy 0)
+                // rows past the end: decay 1, nothing added (channels past the end have x and dy 0)
                 const float dv = live ? d[k * E + i] : 0.f;
                 float g = bg[k].get(i);
                 if constexpr (GATE) {

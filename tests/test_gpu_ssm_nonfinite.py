@@ -53,3 +53,22 @@ def test_a_gradient_that_is_not_finite_stays_in_its_group(dtype, C, S, G, segmen
         same(k, got[k], clean[k])
     want, scale = _ref_scan(c, starts)
     _same_where_finite(got, want, scale, dtype, 150, C, T)
+
+
+@pytest.mark.parametrize("lens,segments", [(None, 0), (None, 2), ([90, 0, 61, 1, 35], 2)])
+@pytest.mark.parametrize("value", [INF, NAN])
+@pytest.mark.parametrize("name", ["x", "delta", "B", "C", "z", "dy", "init", "dfinal"])
+def test_one_value_that_is_not_finite(name, value, lens, segments):
+    """In one sequence, in one row or state: finite exactly where the 64-bit form is, forward and backward, in every output."""
+    N = 5 if lens else 2
+    c, p, starts, T = _scan_case("fp32", 70, 13, 2, N, 90, lens, True, True)
+    if name in ("init", "dfinal"):
+        c[name][N // 2, 3, 5] = value
+    else:
+        row = starts[N // 2] + 40
+        c[name].view(T, -1)[row, 3] = value
+    plan = gcb.ScanPlan(p, segments=segments, segments_backward=segments)
+    print(f"[gpu] scan {name} = {value}, {p}", flush=True)
+    got = _run_scan(plan, c, starts, T)
+    want, scale = _ref_scan(c, starts)
+    _same_where_finite(got, want, scale, "fp32", 90, 70, T)
