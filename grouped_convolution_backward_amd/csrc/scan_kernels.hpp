@@ -111,14 +111,14 @@ __device__ __forceinline__ void write_pairs(f32x2* row, int ec, const float (&a)
     }
 }
 
-// A lane's states' rates, times log2(e) for the hardware's 2^x. Padding
+// A lane's states' rates (decay_rate). Padding
 // states have B = C = 0: they stay 0 and add nothing. Their rate is negative,
 // so that an infinite step is a decay of 0 to them (with a rate of 0 it would
 // be NaN, which 0 times it is too).
 template <int NS>
 __device__ __forceinline__ void load_rates(const ScanArgs& a, int c, bool ok, int s0, float (&A2)[NS]) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) A2[i] = ok && s0 + i < a.S ? a.A[(int64_t)c * a.S + s0 + i] * kLog2e : -1.f;
+    for (int i = 0; i < NS; ++i) A2[i] = ok && s0 + i < a.S ? decay_rate(a.A[(int64_t)c * a.S + s0 + i]) : -1.f;
 }
 template <int NS>
 __device__ __forceinline__ void load_state(const ScanArgs& a, const float* p, int n, int c, bool ok, int s0, float (&h)[NS]) {

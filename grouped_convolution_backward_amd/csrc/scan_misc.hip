@@ -99,7 +99,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(const ScanStepArgs a) {
         hv.load(reinterpret_cast<const Fp32*>(st + i), vec, live ? min(a.S - s0 - i, 4) : 0);
         av.load(reinterpret_cast<const Fp32*>(Ap + i), vec, min(a.S - s0 - i, 4));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[i + j] = hv.get(j), A2[i + j] = av.get(j) * kLog2e;
+        for (int j = 0; j < 4; ++j) h[i + j] = hv.get(j), A2[i + j] = decay_rate(av.get(j));
     }
     Pack<T, 1> xv, dv, zv;
     xv.load(static_cast<const T*>(a.x) + row * a.sx + cc, true, 1);

@@ -278,6 +278,14 @@ __device__ __forceinline__ float exp_neg(float x) {
     return x < -87.f ? e : __builtin_fmaf(e, r * kLn2, e);   // below, p may be infinite and r not a number
 }
 
+// A state's rate, times log2(e) for the hardware's 2^x, at least the lowest
+// finite number: times the step 0, which stands for the rows past a sequence's
+// end, an infinite one would not be the decay 1 but not a number.
+__device__ __forceinline__ float decay_rate(float A) {
+    const float r = A * kLog2e;
+    return r < -3.402823466e38f ? -3.402823466e38f : r;
+}
+
 // The gate's sigmoid: the argument of 2^x rounded as it is, an error of about
 // |z| 2^-24 next to the exact form's 2^-24, at half its instructions.
 __device__ __forceinline__ float gate_sigmoid(float z) {

@@ -121,7 +121,7 @@ int wgrad_cconv_step_run(const wgrad_cconv_plan_t* plan, const wgrad_cconv_args*
  * h starts as init_state[n] (or 0) and ends as final_state[n]. delta_bias, D
  * and z are optional (0, 0 and no gate). Rows of B and C hold G groups of S
  * values. States, exponentials and sums are fp32; an exponential below 2^-126
- * counts as 0.
+ * counts as 0, and a rate A below -2.3e38 (-infinity too) as -2.3e38.
  */
 typedef struct {
     int32_t dtype;     /* wgrad_dtype of x, delta, B, C, z, y and their gradients */

@@ -72,3 +72,24 @@ def test_one_value_that_is_not_finite(name, value, lens, segments):
     got = _run_scan(plan, c, starts, T)
     want, scale = _ref_scan(c, starts)
     _same_where_finite(got, want, scale, "fp32", 90, 70, T)
+
+
+@pytest.mark.parametrize("dtype,S,segments", [("fp32", 16, 0), ("fp32", 13, 2), ("bf16", 40, 2)])
+def test_a_rate_of_minus_infinity_keeps_nothing(dtype, S, segments):
+    """Such a state is d x B of the row alone: in the last row too, whose tile ends past the sequence, and in the gradients,
+    where it counts as the lowest finite rate."""
+    L = 75
+    c, p, starts, T = _scan_case(dtype, 20, S, 1, 2, L, None, True, True)
+    c["A"][3, 5], c["A"][7, 0] = -INF, -3e38
+    plan = gcb.ScanPlan(p, segments=segments, segments_backward=segments)
+    got = _run_scan(plan, c, starts, T)
+    limit = dict(c, A=c["A"].clamp(min=-1e30))
+    want, scale = _ref_scan(limit, starts)
+    _same_where_finite(got, want, {k: v.nan_to_num() for k, v in scale.items()}, dtype, L, 20, T)
+    state = torch.randn(2, 20, S, generator=torch.Generator().manual_seed(1)).cuda()
+    y = torch.empty(2, 20, dtype=ref.TORCH[dtype], device="cuda")
+    d = {k: v.cuda() for k, v in c.items()}
+    plan.run_step(d["x"][:2], d["delta"][:2], d["A"], d["B"][:2], d["C"][:2], state, y, D=d["D"], z=d["z"][:2],
+                  delta_bias=d["bias"])
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(state).all())
