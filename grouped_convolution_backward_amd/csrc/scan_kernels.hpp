@@ -147,6 +147,16 @@ __device__ __forceinline__ void store_quads(float* p, const float (&h)[NS]) {
     for (int i = 0; i < NS; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{h[i], h[i + 1], h[i + 2], h[i + 3]};
 }
 
+// A state h carried over a segment whose decays multiply to 2^p and whose own
+// sum is s. The factor is applied in two halves, each finite: it may be beyond
+// fp32 where the carried state is small enough, or 0, and its product is not
+// (growing states). Beyond 2^255.98 any state but 0 overflows as it would row
+// by row. p is not a number only if s is none either.
+__device__ __forceinline__ float carry(float p, float h, float s) {
+    const float f = __builtin_amdgcn_exp2f(__builtin_fminf(0.5f * p, 127.99f));
+    return __builtin_fmaf(f * h, f, s);
+}
+
 // The record of the states before row t (a multiple of kChunk) of a sequence.
 __device__ __forceinline__ int64_t saved_slot(const ScanArgs& a, const Piece& pc, int t) {
     const int base = a.pc.seq_start ? pc.row0 / kChunk + pc.n : pc.n * ((a.pc.L + kChunk - 1) / kChunk);
@@ -270,7 +280,7 @@ __global__ __launch_bounds__(256) void fwd_kernel(const ScanArgs a) {
             float s[NS];
             load_quads<NS>(a.sums + rec * SP + s0, s);
 #pragma unroll
-            for (int i = 0; i < NS; ++i) h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[i] * sd), h[i], s[i]);
+            for (int i = 0; i < NS; ++i) h[i] = carry(A2[i] * sd, h[i], s[i]);
         }
     }
     float sum_d = 0.f;
@@ -610,7 +620,7 @@ __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(co
             float s[NS];
             load_quads<NS>(a.sums + rec * SP + s0, s);
 #pragma unroll
-            for (int i = 0; i < NS; ++i) e[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[i] * sd), e[i], s[i]);
+            for (int i = 0; i < NS; ++i) e[i] = carry(A2[i] * sd, e[i], s[i]);
         }
         // lanes past the block's last channel read another channel's records: their e enters the sums over channels, where 0
         // times it is not 0 if it is infinite

@@ -93,3 +93,52 @@ def test_a_rate_of_minus_infinity_keeps_nothing(dtype, S, segments):
                   delta_bias=d["bias"])
     torch.cuda.synchronize()
     assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(state).all())
+
+
+def _growing(S, L, segments):
+    c, p, starts, T = _scan_case("fp32", 24, S, 1, 1, L, None, True, True)
+    c["delta"].fill_(1.0)
+    c["bias"].zero_()
+    c["A"] = -c["A"].abs().clamp(max=4.0)
+    c["A"][:, ::2] = 2.8                                    # over 32 rows e^89.6, above what fp32 holds
+    plan = gcb.ScanPlan(dict(p, softplus=False), segments=segments, segments_backward=segments)
+    assert plan.info["segments"] == plan.info["segments_backward"] and (plan.info["segments"] > 1) == (segments > 1)
+    return c, starts, T, plan
+
+
+@pytest.mark.parametrize("S,segments", [(16, 1), (16, 4), (5, 3), (40, 4), (100, 2)])
+def test_growing_states_that_are_still_zero(S, segments):
+    """Rates above 0 over segments whose decays multiply to more than fp32 holds, while the state (from its start) and its
+    gradient (from its end) are still 0: a split must not make NaN of infinity times 0."""
+    L = 120
+    c, starts, T, plan = _growing(S, L, segments)
+    c["x"][:100], c["dy"][20:] = 0.0, 0.0
+    c["init"].zero_()
+    c["dfinal"].zero_()
+    got = _run_scan(plan, c, starts, T)
+    want, scale = _ref_scan(c, starts, softplus=False)
+    _same_where_finite(got, want, scale, "fp32", L, 24, T)
+
+
+@pytest.mark.parametrize("S,segments", [(16, 1), (16, 2), (5, 2), (40, 2), (100, 2)])
+def test_growing_states_from_very_small_ones(S, segments):
+    """The same from a state of 1e-36, and a gradient of it: 60 rows end below 1e38, though one segment's decays alone
+    multiply to more than fp32 holds."""
+    L = 60
+    c, starts, T, plan = _growing(S, L, segments)
+    c["C"] *= 0.01
+    c["init"].fill_(1e-36)
+    c["x"].zero_()
+    c["dy"].zero_()
+    c["dfinal"].zero_()
+    want, scale = _ref_scan(c, starts, softplus=False)
+    got = _run_scan(plan, c, starts, T)
+    assert float(want["final_state"].max()) > 1e36
+    _same_where_finite(got, want, scale, "fp32", L, 24, T)
+    c["init"].zero_()
+    c["dfinal"].fill_(1e-36)
+    c["B"] *= 0.01
+    want, scale = _ref_scan(c, starts, softplus=False)
+    got = _run_scan(plan, c, starts, T)
+    assert float(want["dinit_state"].max()) > 1e36
+    _same_where_finite(got, want, scale, "fp32", L, 24, T)
