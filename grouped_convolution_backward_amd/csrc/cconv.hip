@@ -219,8 +219,20 @@ __global__ __launch_bounds__(256) void cconv_bwd_kernel(const CconvArgs a) {
                 for (int k = 0; k < W; ++k) dx[i] = __builtin_fmaf(w[k][i], gw[W - 1 - k][i], dx[i]);
             }
         };
+        // dx of row s - (W - 1) again at a sequence's ends, from its own rows only: a weight times the 0 that stands for the
+        // gradient of another row is not 0 if the weight is infinite
+        auto inner = [&](int s, float (&dx)[E]) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                dx[i] = 0.f;
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    if (s - k >= 0 && s - k < pc.len) dx[i] = __builtin_fmaf(w[k][i], gw[W - 1 - k][i], dx[i]);
+            }
+        };
         const int fin = a.dfinal ? pc.len - (W - 1) : 1 << 30;   // rows from here on are in the final state too
         auto finish = [&](int r, float (&dx)[E]) {         // r: the row whose dx is complete
+            if (r < 0 && starts) inner(r + W - 1, dx);
             if (r >= fin) {
                 Pack<T, E> v;
                 v.load(static_cast<const T*>(a.dfinal) + ((int64_t)pc.n * (W - 1) + r - fin) * a.C + c, VEC, nv);
@@ -266,12 +278,8 @@ __global__ __launch_bounds__(256) void cconv_bwd_kernel(const CconvArgs a) {
                 advance(nx[u], nd[u], dx);
                 if (r >= pc.len) {                         // past the sequence: no gradient, whatever a state's NaN made of it
 #pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        gw[W - 1][i] = 0.f;
-                        dx[i] = 0.f;
-#pragma unroll
-                        for (int k = 1; k < W; ++k) dx[i] = __builtin_fmaf(w[k][i], gw[W - 1 - k][i], dx[i]);
-                    }
+                    for (int i = 0; i < E; ++i) gw[W - 1][i] = 0.f;
+                    inner(r, dx);
                 }
                 if (r < end) {
 #pragma unroll

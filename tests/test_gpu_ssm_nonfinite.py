@@ -8,7 +8,8 @@ torch = pytest.importorskip("torch")
 gcb = pytest.importorskip("grouped_convolution_backward_amd")
 
 import ssm_reference as ref  # noqa: E402
-from test_gpu_ssm import _ref_scan, _run_scan, _scan_case  # noqa: E402
+from test_gpu_ssm import (_conv_case, _nan, _nan_bytes, _ref_conv, _ref_scan, _run_scan, _scan_case,  # noqa: E402
+                          _seq_start)
 
 pytestmark = pytest.mark.gpu
 
@@ -142,3 +143,36 @@ def test_growing_states_from_very_small_ones(S, segments):
     got = _run_scan(plan, c, starts, T)
     assert float(want["dinit_state"].max()) > 1e36
     _same_where_finite(got, want, scale, "fp32", L, 24, T)
+
+
+@pytest.mark.parametrize("lens", [None, [40, 0, 33, 1, 2, 38]])
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+@pytest.mark.parametrize("name", ["x", "dy", "init", "dfinal", "w", "bias"])
+@pytest.mark.parametrize("dtype,C,W,act", [("bf16", 36, 4, "silu"), ("fp32", 7, 8, "silu"), ("fp16", 1, 3, "none")])
+def test_one_value_of_the_convolution_that_is_not_finite(dtype, C, W, act, name, value, lens):
+    """Finite exactly where the 64-bit form is, in every output of forward and backward."""
+    N, L = (6, 40) if lens else (3, 40)
+    c, p, starts, T = _conv_case(dtype, C, W, N, L, lens, act, True, 0)
+    at = {"x": (starts[2] + 12, C - 1), "dy": (starts[2] + 12, C - 1), "init": (2, W - 2, C - 1), "dfinal": (2, W - 2, C - 1),
+          "w": (C - 1, 1), "bias": (C - 1,)}[name]
+    c[name][at] = value
+    want, scale = _ref_conv(c, starts, act)
+    plan = gcb.CausalConvPlan(p)
+    print(f"[gpu] conv {name} = {value}, {p}", flush=True)
+    d = {k: v.cuda() for k, v in c.items()}
+    seq = {"seq_start": _seq_start(starts)} if lens else {}
+    y, final, dx = _nan(T, C, dtype=dtype), _nan(N, W - 1, C, dtype=dtype), _nan(T, C, dtype=dtype)
+    dw, db, dinit = _nan(C, W), _nan(C), _nan(N, W - 1, C, dtype=dtype)
+    plan.run(d["x"], d["w"], y, bias=d["bias"], init_state=d["init"], final_state=final, **seq)
+    plan.run_backward(d["x"], d["w"], d["dy"], dx, dw, dbias=db, bias=d["bias"], init_state=d["init"], dinit_state=dinit,
+                      dfinal_state=d["dfinal"], ws=_nan_bytes(plan.workspace_bytes), **seq)
+    torch.cuda.synchronize()
+    got = {"y": y, "final_state": final, "dx": dx, "dinit_state": dinit, "dw": dw, "dbias": db}
+    for k, v in got.items():
+        g, w, s = v.double().cpu().reshape(-1), want[k].reshape(-1), scale[k].reshape(-1)
+        fine = torch.isfinite(w)
+        assert torch.equal(torch.isfinite(g), fine), f"{k}: {int((torch.isfinite(g) != fine).sum())} of {g.numel()} values"
+        if k == "final_state":
+            same(k, g[fine], w[fine])
+        else:
+            ref.assert_close(k, g[fine], w[fine], s[fine], "fp32" if k in ("dw", "dbias") else dtype, 2 * W + 24 + T)
