@@ -595,6 +595,10 @@ __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(co
     __shared__ __attribute__((aligned(16))) float sB[K][SP];
     __shared__ __attribute__((aligned(16))) float sC[K][SP];
     __shared__ float sP[4][K][2 * SP + CS::kLeft];   // a row's last places: from lanes that hold nothing of use
+    // Sums over rows that each lane keeps for itself. A running sum over a long
+    // segment would round as often as it has chunks (dD over 16384 rows, fp32:
+    // 5.2e-7 off); each 16 chunks' sums are added here instead (1.7e-7).
+    __shared__ float sSum[2 * E][256];
 
     const int nblk = a.cblks_g * a.G;
     const int id = blockIdx.x / nblk;
@@ -639,6 +643,8 @@ __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(co
     float dD[E], dbias[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) dD[i] = dbias[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2 * E; ++i) sSum[i][tid] = 0.f;
     // channels past the end: no lane stages every one of them, all are summed over
     for (int i = tid; i < K * CT; i += 256) (&sIn[0][0])[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (tid < CT) {
@@ -835,6 +841,13 @@ __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(co
                 dbias[i] += live ? dr : 0.f;
             }
         }
+        if ((t0 / K) % 16 == 0) {                          // the last of them at t0 = 0
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                sSum[i][tid] += dD[i], dD[i] = 0.f;
+                sSum[E + i][tid] += dbias[i], dbias[i] = 0.f;
+            }
+        }
         // The next chunk is staged before this one's rows are stored: loads and
         // stores retire in order, so a wait for the chunk's loads behind fresh
         // stores would wait for those to reach memory.
@@ -865,8 +878,8 @@ __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(co
     float* const sR = reinterpret_cast<float*>(&sIn[0][0]);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-        sR[et * CT + ec + i] = dD[i];
-        sR[(RK + et) * CT + ec + i] = dbias[i];
+        sR[et * CT + ec + i] = sSum[i][tid];
+        sR[(RK + et) * CT + ec + i] = sSum[E + i][tid];
     }
     lds_barrier();
     for (int w = tid; w < 2 * CT; w += 256) {

@@ -12,8 +12,8 @@ using scan::f32x4;
 
 // Three jobs side by side in one launch, each summing partials in one order:
 // dB and dC over the channel blocks of a group, dA over the pieces, dD and
-// ddelta_bias over the pieces. Consecutive lanes read consecutive words; the
-// loops are unrolled for their loads, which do not wait for the sum (8192 rows,
+// ddelta_bias over the pieces. Consecutive lanes read consecutive words, 16
+// loads at a time, which do not wait for the sum (8192 rows,
 // 16 states, 64 channel blocks: 13.9 us for 70 MB, which the caches hold).
 template <class T>
 __global__ __launch_bounds__(256) void scan_reduce_kernel(const ScanReduceArgs a, int64_t n_bc, int64_t n_a) {
@@ -28,11 +28,8 @@ __global__ __launch_bounds__(256) void scan_reduce_kernel(const ScanReduceArgs a
         if (s >= a.S) return;
         const float* p = a.part_bc + ((int64_t)g * a.cblks_g * a.rows + row) * W + s2;
         const int64_t step = (int64_t)a.rows * W;
-        float v = 0.f;
-#pragma unroll 8
-        for (int k = 0; k < a.cblks_g; ++k) v += p[k * step];
         Pack<T, 1> out;
-        out.set(0, v);
+        out.set(0, sum_of(a.cblks_g, [&](int k) { return p[k * step]; }));
         T* d = s2 < a.SP ? static_cast<T*>(a.dB) + row * a.sdB : static_cast<T*>(a.dC) + row * a.sdC;
         out.store(d + (int64_t)g * a.S + s, true, 1);
         return;
@@ -42,10 +39,7 @@ __global__ __launch_bounds__(256) void scan_reduce_kernel(const ScanReduceArgs a
         const int s = (int)(i % a.SP);
         const int64_t c = i / a.SP;
         if (s >= a.S) return;
-        float v = 0.f;
-#pragma unroll 8
-        for (int p = 0; p < a.pieces; ++p) v += a.part_a[((int64_t)p * a.channels + c) * a.SP + s];
-        a.dA[c * a.S + s] = v;
+        a.dA[c * a.S + s] = sum_of(a.pieces, [&](int p) { return a.part_a[((int64_t)p * a.channels + c) * a.SP + s]; });
         return;
     }
     i -= n_a;
@@ -54,10 +48,7 @@ __global__ __launch_bounds__(256) void scan_reduce_kernel(const ScanReduceArgs a
     const int64_t c = i - (which ? a.channels : 0);
     float* out = which ? a.ddelta_bias : a.dD;
     if (!out) return;
-    float v = 0.f;
-#pragma unroll 8
-    for (int p = 0; p < a.pieces; ++p) v += a.part_d[((int64_t)p * 2 + which) * a.channels + c];
-    out[c] = v;
+    out[c] = sum_of(a.pieces, [&](int p) { return a.part_d[((int64_t)p * 2 + which) * a.channels + c]; });
 }
 
 template <class T>

@@ -335,5 +335,31 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
+// The sum of value(0) .. value(n - 1) in one order, in levels of 16: a running
+// sum's roundings grow with the root of its terms, these with that of a few
+// tens. 16 values are asked for at a time, so that their loads go out together.
+template <class F>
+__device__ __forceinline__ float sum_of(int n, F value) {
+    float all = 0.f;
+    for (int a = 0; a < n; a += 256) {
+        float some = 0.f;
+        for (int b = a; b < min(n, a + 256); b += 16) {
+            float few = 0.f;
+            if (b + 16 <= n) {
+                float v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = value(b + k);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) few += v[k];
+            } else {
+                for (int k = b; k < n; ++k) few += value(k);
+            }
+            some += few;
+        }
+        all += some;
+    }
+    return all;
+}
+
 }  // namespace ssm
 }  // namespace wgrad
