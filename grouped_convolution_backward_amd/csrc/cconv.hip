@@ -313,8 +313,7 @@ __global__ __launch_bounds__(256) void cconv_bwd_kernel(const CconvArgs a) {
         if (slot == 0 && nv > 0) {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                float v = part[lane][i];
-                for (int s = 1; s < 256 / cl; ++s) v += part[s * cl + lane][i];
+                const float v = sum_of(256 / cl, [&](int s) { return part[s * cl + lane][i]; });
                 if (i < nv) a.part[((int64_t)id * (W + 1) + k) * a.C + c + i] = v;
             }
         }
@@ -323,13 +322,13 @@ __global__ __launch_bounds__(256) void cconv_bwd_kernel(const CconvArgs a) {
 }
 
 // dw and dbias from the pieces' partials: 32 channels of one tap per
-// workgroup, the pieces dealt to 8 lanes each and joined in one order.
+// workgroup, the pieces dealt to 8 lanes each and joined in one order, in
+// levels (65536 sequences of 8 rows, fp32: dw 1.5e-6 off as a running sum).
 __global__ __launch_bounds__(256) void cconv_reduce_kernel(const CconvReduceArgs a) {
     const int k = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
     float v = 0.f;
     if (c < a.C)
-#pragma unroll 8
-        for (int p = sl; p < a.pieces; p += 8) v += a.part[((int64_t)p * (a.W + 1) + k) * a.C + c];
+        v = sum_of((a.pieces - sl + 7) / 8, [&](int p) { return a.part[((int64_t)(8 * p + sl) * (a.W + 1) + k) * a.C + c]; });
     __shared__ float part[256];
     part[threadIdx.x] = v;
     __syncthreads();

@@ -337,28 +337,32 @@ __device__ __forceinline__ float lanes_sum(float v) {
 
 // The sum of value(0) .. value(n - 1) in one order, in levels of 16: a running
 // sum's roundings grow with the root of its terms, these with that of a few
-// tens. 16 values are asked for at a time, so that their loads go out together.
+// tens. Values are asked for 16, 8 and 4 at a time, so that their loads go out
+// together.
+template <int K, class F>
+__device__ __forceinline__ void add_values(float& sum, int& at, F value) {
+    float v[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = value(at + k);
+#pragma unroll
+    for (int k = 0; k < K; ++k) sum += v[k];
+    at += K;
+}
 template <class F>
 __device__ __forceinline__ float sum_of(int n, F value) {
-    float all = 0.f;
-    for (int a = 0; a < n; a += 256) {
-        float some = 0.f;
-        for (int b = a; b < min(n, a + 256); b += 16) {
-            float few = 0.f;
-            if (b + 16 <= n) {
-                float v[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = value(b + k);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) few += v[k];
-            } else {
-                for (int k = b; k < n; ++k) few += value(k);
-            }
-            some += few;
-        }
-        all += some;
+    float all = 0.f, some = 0.f, few = 0.f;
+    int at = 0;
+    while (n - at >= 16) {
+        few = 0.f;
+        add_values<16>(few, at, value);
+        some += few;
+        if (at % 256 == 0) all += some, some = 0.f;
     }
-    return all;
+    few = 0.f;
+    if (n - at >= 8) add_values<8>(few, at, value);
+    if (n - at >= 4) add_values<4>(few, at, value);
+    while (at < n) add_values<1>(few, at, value);
+    return all + (some + few);
 }
 
 }  // namespace ssm

@@ -15,7 +15,7 @@ torch = pytest.importorskip("torch")
 gcb = pytest.importorskip("grouped_convolution_backward_amd")
 
 import ssm_reference as ref  # noqa: E402
-from test_gpu_ssm import _conv_case, _nan, _nan_bytes, _run_scan, _scan_case  # noqa: E402
+from test_gpu_ssm import _nan, _nan_bytes, _run_scan, _scan_case  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,22 @@ def test_scan_parameter_gradients_over_many_rows(S, N, L):
     off = {k: _off(got[k], want[k]) for k in ("dD", "ddelta_bias", "dA")}
     print(off, flush=True)
     assert off["dD"] < 4e-7 and off["ddelta_bias"] < 6e-7 and off["dA"] < 1e-6, off
+
+
+@pytest.mark.parametrize("N,L,C,W", [(65536, 8, 64, 4), (4096, 64, 256, 4), (1, 2 ** 18, 4, 3)])
+def test_convolution_parameter_gradients_over_many_rows(N, L, C, W):
+    g = torch.Generator().manual_seed(N + L)
+    x, dy = torch.randn(N, L, C, generator=g), torch.randn(N, L, C, generator=g)
+    w, b = torch.randn(C, W, generator=g) * 0.6, torch.randn(C, generator=g) * 0.3
+    plan = gcb.CausalConvPlan({"dtype": "fp32", "N": N, "L": L, "C": C, "W": W, "activation": "silu"})
+    dx, dw, db = _nan(N, L, C), _nan(C, W), _nan(C)
+    print(f"[gpu] conv {plan.problem}", flush=True)
+    plan.run_backward(x.cuda(), w.cuda(), dy.cuda(), dx, dw, dbias=db, bias=b.cuda(), ws=_nan_bytes(plan.workspace_bytes))
+    torch.cuda.synchronize()
+    line = torch.cat([torch.zeros(N, W - 1, C), x], 1).double()
+    p = b.double() + sum(line[:, k:k + L] * w[:, k].double() for k in range(W))
+    s = dy.double() * ref.dsilu(p)
+    want = torch.stack([(s * line[:, k:k + L]).sum((0, 1)) for k in range(W)], 1)
+    off = {"dw": _off(dw, want), "dbias": _off(db, s.sum((0, 1)))}
+    print(off, flush=True)
+    assert off["dw"] < 4e-7 and off["dbias"] < 4e-7, off
