@@ -258,8 +258,9 @@ __global__ __launch_bounds__(256) void fwd_kernel(const ScanArgs a) {
     __shared__ __attribute__((aligned(16))) float sC[TT][SP];
 
     const int nblk = a.cblks_g * a.G;
-    const int id = blockIdx.x / nblk;
-    const Block cb = channel_block<scan_unit(LPC)>(a, blockIdx.x - id * nblk);
+    const int group = workgroup(), id = group / nblk;
+    if (id >= a.pc.count) return;
+    const Block cb = channel_block<scan_unit(LPC)>(a, group - id * nblk);
     const Piece pc = find_piece(a.pc, id);
     if (SUM ? (pc.rows <= 0 || pc.last) : (pc.rows <= 0 && !pc.last)) return;
 
@@ -428,8 +429,9 @@ __global__ __launch_bounds__(256) void bwd_sum_kernel(const ScanArgs a) {
     __shared__ __attribute__((aligned(16))) float sC[TT][SP];
 
     const int nblk = a.cblks_g * a.G;
-    const int id = blockIdx.x / nblk;
-    const Block cb = channel_block<scan_unit(LPC)>(a, blockIdx.x - id * nblk);
+    const int group = workgroup(), id = group / nblk;
+    if (id >= a.pc.count) return;
+    const Block cb = channel_block<scan_unit(LPC)>(a, group - id * nblk);
     const Piece pc = find_piece(a.pc, id);
     if (pc.rows <= 0 || pc.j == 0) return;
 
@@ -601,8 +603,9 @@ __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(co
     __shared__ float sSum[2 * E][256];
 
     const int nblk = a.cblks_g * a.G;
-    const int id = blockIdx.x / nblk;
-    const Block cb = channel_block<scan_unit(LPC)>(a, blockIdx.x - id * nblk);
+    const int group = workgroup(), id = group / nblk;
+    if (id >= a.pc.count) return;
+    const Block cb = channel_block<scan_unit(LPC)>(a, group - id * nblk);
     const Piece pc = find_piece(a.pc, id);
     const int rows = max(pc.rows, 0);
 
@@ -894,14 +897,14 @@ __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(co
 
 template <class T, int NS, int LPC, int VEC>
 int run_fwd(const ScanArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)(a.pc.count * a.cblks_g * a.G));
+    const dim3 grid = launch_grid((int64_t)a.pc.count * a.cblks_g * a.G);
     if (a.split) fwd_kernel<T, NS, LPC, VEC, true><<<grid, 256, 0, s>>>(a);
     fwd_kernel<T, NS, LPC, VEC, false><<<grid, 256, 0, s>>>(a);
     return (int)hipGetLastError();
 }
 template <class T, int NS, int LPC, int VEC>
 int run_bwd(const ScanArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)(a.pc.count * a.cblks_g * a.G));
+    const dim3 grid = launch_grid((int64_t)a.pc.count * a.cblks_g * a.G);
     if (a.split) bwd_sum_kernel<T, NS, LPC, VEC><<<grid, 256, 0, s>>>(a);
     if (a.z)
         bwd_kernel<T, NS, LPC, VEC, true><<<grid, 256, 0, s>>>(a);

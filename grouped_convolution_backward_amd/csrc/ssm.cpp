@@ -237,7 +237,7 @@ int build_scan(const wgrad_scan_problem& p, const wgrad_scan_overrides* ov, cons
     const int64_t chunks = p.packed ? (p.N ? T / kChunk + p.N : 0) : p.N * ceil_div(p.L, kChunk);
     info.saved_bytes = chunks * p.C * SP * 4;
     const int64_t sums = p.C * (SP + 1) * 4;
-    if (T * p.G * 2 * SP / 256 + p.C * (SP + 2) / 256 + 1 > kMaxGrid) return invalid("problem too large for one launch");
+    if (ceil_div(T * p.G * 2 * SP + p.C * (SP + 2), 256) > kMaxGrid) return invalid("problem too large for one launch");
     // every part starts on 16 bytes: the quads (sums, part_bc, part_a) come first
     info.workspace_bytes = out.fwd.split ? (int64_t)out.fwd.pc.count * sums : 0;
     info.workspace_bytes_backward = nblk * T * 2 * SP * 4 + (int64_t)out.bwd.pc.count * (p.C * SP * 4 + 2 * p.C * 4) +

@@ -45,6 +45,15 @@ constexpr PieceRows piece_rows(int32_t j, int32_t len, int32_t rows) {
     return {t0, left < rows ? left : rows, some && (j == 0 ? len <= rows : left > 0 && left <= rows)};
 }
 
+// The grid of a launch. Work items along one axis have to stay below 2^32 (a
+// larger grid is cut off without an error), so workgroups of 256 beyond 2^20
+// lie in rows of 2^20; those of the last row that are too many leave at once.
+constexpr int64_t kGridRow = int64_t(1) << 20;
+struct Grid { uint32_t x, y; };
+constexpr Grid grid_of(int64_t workgroups) {
+    return {(uint32_t)(workgroups < kGridRow ? workgroups : kGridRow), (uint32_t)((workgroups + kGridRow - 1) / kGridRow)};
+}
+
 // The byte offset, from row `base` of a tensor on, of place `at` in row t. For
 // rows that are not accessed (their offsets go out of range afterwards) it is
 // any number, so it is formed modulo 2^32. Host and device.
