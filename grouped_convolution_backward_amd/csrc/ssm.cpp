@@ -58,6 +58,8 @@ int check_sequences(int packed, int64_t N, int64_t L, int64_t& T) {
         T = rows;
     } else if (N == 0 && T != 0) {
         return invalid("packed rows without a sequence");
+    } else if (T > N * L) {
+        return invalid("T must be at most N * L: no sequence is longer than L");
     }
     return WGRAD_OK;
 }

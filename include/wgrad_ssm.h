@@ -61,7 +61,7 @@ typedef struct {
     int32_t W;          /* filter taps, 1 to 8 */
     int32_t packed;     /* 0 or 1 */
     int64_t N, L;       /* sequences >= 0, rows per sequence (packed: at most) >= 0 */
-    int64_t T;          /* packed: rows in all; dense: 0 or N*L */
+    int64_t T;          /* packed: rows in all, at most N*L; dense: 0 or N*L */
     int64_t C;          /* channels >= 1 */
 } wgrad_cconv_problem;
 
