@@ -20,8 +20,9 @@ take seq_start, an int32 GPU tensor of N + 1; W and activation ("none",
 "silu") of a convolution; S states, G groups (1) and softplus (True) of a
 scan. Activations are [N, L, C] or [T, C] (B and C: [..., G, S] or, for one
 group, [..., S]); rows may have a stride, as the halves of a wider matrix do,
-elements of a row are adjacent. A tensor that does not fit is a ValueError,
-what the library refuses a WgradError.
+elements of a row are adjacent. Neighbouring axes may be merged or split, and
+axes of 1 added. A tensor that does not fit is a ValueError, what the library
+refuses a WgradError.
 """
 
 from __future__ import annotations
@@ -112,6 +113,34 @@ def declare(lib):
     lib.wgrad_scan_plan_query.argtypes, lib.wgrad_scan_plan_query.restype = [_vp, P(wgrad_scan_plan_info)], ctypes.c_int
 
 
+def _same_order(shape, want):
+    """Whether a tensor of `shape` holds the elements of one of shape `want` in the same order: its axes, or some of them
+    merged, or split, wherever axes of 1 stand. Then the ends of the one's axes are among the ends of the other's."""
+    def ends(dims):
+        n, at = 1, set()
+        for v in dims:
+            n *= v
+            at.add(n)
+        return n, at - {1}
+    (n, a), (m, b) = ends(shape), ends(want)
+    return n == m and (n == 0 or a <= b or b <= a)
+
+
+class _Form:
+    """The shape that an operand has to have, and the shapes that have been found to hold it."""
+
+    __slots__ = ("shape", "rows", "width", "known")
+
+    def __init__(self, *shape, rows=None):
+        self.shape, self.known = shape, set()
+        self.rows = rows
+        if rows is not None:                                # a row operand: `rows` rows of `width` elements
+            self.width = 1
+            for v in shape:
+                self.width *= v
+            self.width = self.width // rows if rows else 0
+
+
 def _gcb():
     import grouped_convolution_backward_amd as gcb
     return gcb
@@ -147,7 +176,10 @@ class _SsmPlan:
         # the current stream's handle without a Stream object around it, where this torch offers that
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        # the current device's number, likewise without the check that the GPU is initialised: operands are on it
+        self._current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         self._strides = {}          # row stride by (shape, strides, row width) of strided operands
+        self._step_forms = {}       # forms of a step's operands by (rows, states)
 
     def close(self):
         if getattr(self, "handle", None) is not None and self.handle.value:
@@ -164,18 +196,27 @@ class _SsmPlan:
     def _block(self, x):
         """An empty block and the device that every operand has to be on: x's, which has to be the current one."""
         dev = x.get_device()
-        if dev < 0 or dev != self._torch.cuda.current_device():
+        if dev < 0 or dev != self._current():
             raise ValueError(f"x: need a tensor on the current GPU (got one on {x.device})")
         return [0] * self._words, dev
 
-    def _rows_of(self, w, dev, name, t, rows, width):
-        """A row operand: rows of `width` adjacent elements at one distance."""
-        if t.dtype is not self.dtype or t.get_device() != dev or t.numel() != rows * width:
-            raise ValueError(f"{name}: need a {self.dtype} tensor on cuda:{dev}, the current device, with {rows} rows of {width} "
-                             f"elements (got {t.dtype}, {tuple(t.shape)} on {t.device})")
+    def _look(self, name, t, form, dtype, dev):
+        """t is not known to fit `form`: a ValueError, or its shape is known from now on."""
+        if t.dtype is not dtype or t.get_device() != dev or not _same_order(t.shape, form.shape):
+            raise ValueError(f"{name}: need a {dtype} tensor of shape {form.shape} on cuda:{dev}, the current device (got "
+                             f"{t.dtype}, {tuple(t.shape)} on {t.device})")
+        if len(form.known) >= 16:
+            form.known.clear()
+        form.known.add(t.shape)
+
+    def _rows_of(self, w, dev, name, t, form):
+        """A row operand: rows of adjacent elements at one distance."""
+        if t.dtype is not self.dtype or t.shape not in form.known or t.get_device() != dev:
+            self._look(name, t, form, self.dtype, dev)
         i = self._at[name]
         w[i] = t.data_ptr()
-        if t.is_contiguous() or rows == 0:
+        width = form.width
+        if t.is_contiguous() or form.rows == 0:
             w[i + 1] = width
             return
         key = (t.shape, t.stride(), width)
@@ -208,8 +249,18 @@ class _SsmPlan:
             span *= shape[i]
         return step if span > 1 else width
 
-    def _dense(self, w, dev, name, t, numel, dtype):
+    def _dense(self, w, dev, name, t, form, dtype):
         """A contiguous operand; None is a null pointer."""
+        if t is None:
+            return
+        if t.dtype is not dtype or t.shape not in form.known or t.get_device() != dev:
+            self._look(name, t, form, dtype, dev)
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: need a contiguous tensor (strides {tuple(t.stride())} of shape {tuple(t.shape)})")
+        w[self._at[name]] = t.data_ptr()
+
+    def _vector(self, w, dev, name, t, numel, dtype):
+        """A contiguous operand of one axis; None is a null pointer."""
         if t is None:
             return
         if t.dtype is not dtype or t.get_device() != dev or t.numel() != numel or not t.is_contiguous():
@@ -217,11 +268,23 @@ class _SsmPlan:
                              f"(got {t.dtype}, {tuple(t.shape)} on {t.device})")
         w[self._at[name]] = t.data_ptr()
 
+    def _lead(self):
+        """The axes over rows of whole sequences."""
+        p = self._struct
+        return (int(p.T),) if p.packed else (int(p.N), int(p.L))
+
+    def _new_step(self, rows, pool, *forms):
+        """The forms of a step's operands, kept by its rows and states."""
+        if len(self._step_forms) >= 64:
+            self._step_forms.clear()
+        self._step_forms[rows, pool] = forms
+        return forms
+
     def _seq(self, w, dev, seq_start):
         p = self._struct
         if bool(p.packed) != (seq_start is not None):
             raise ValueError("seq_start belongs to packed problems, and only to them")
-        self._dense(w, dev, "seq_start", seq_start, p.N + 1, self._torch.int32)
+        self._vector(w, dev, "seq_start", seq_start, p.N + 1, self._torch.int32)
 
     def _buffer(self, w, dev, name, t, need):
         if t is None or t.get_device() != dev or not t.is_contiguous() or t.numel() * t.element_size() < need:
@@ -235,7 +298,7 @@ class _SsmPlan:
 
     def _slots(self, w, dev, slots, rows, pool):
         w[self._at["rows"]], w[self._at["num_slots"]] = rows, pool
-        self._dense(w, dev, "slots", slots, rows, self._torch.int32)
+        self._vector(w, dev, "slots", slots, rows, self._torch.int32)
 
     def _call(self, f, w, dev, stream):
         if stream is None:
@@ -260,7 +323,9 @@ class CausalConvPlan(_SsmPlan):
     def __init__(self, problem: dict, hip_device: int | None = None):
         super().__init__(problem, hip_device)
         p = self._struct
-        self._C, self._W, self._state_numel = int(p.C), int(p.W), int(p.N * (p.W - 1) * p.C)
+        C, W = self._C, self._W = int(p.C), int(p.W)
+        self._row_form, self._taps = _Form(*self._lead(), C, rows=self.rows), _Form(C, W)
+        self._states = _Form(int(p.N), W - 1, C)
         self.workspace_bytes = int(self._lib.wgrad_cconv_workspace_bytes(self.handle))
 
     @staticmethod
@@ -279,28 +344,28 @@ class CausalConvPlan(_SsmPlan):
         return self._bytes(self.workspace_bytes, device)
 
     def run(self, x, w, y, bias=None, init_state=None, final_state=None, seq_start=None, stream=None):
-        (a, dev), C, t = self._block(x), self._C, self.dtype
-        self._rows_of(a, dev, "x", x, self.rows, C)
-        self._rows_of(a, dev, "y", y, self.rows, C)
-        self._dense(a, dev, "w", w, C * self._W, t)
-        self._dense(a, dev, "bias", bias, C, t)
-        self._dense(a, dev, "init_state", init_state, self._state_numel, t)
-        self._dense(a, dev, "final_state", final_state, self._state_numel, t)
+        (a, dev), C, t, rows = self._block(x), self._C, self.dtype, self._row_form
+        self._rows_of(a, dev, "x", x, rows)
+        self._rows_of(a, dev, "y", y, rows)
+        self._dense(a, dev, "w", w, self._taps, t)
+        self._vector(a, dev, "bias", bias, C, t)
+        self._dense(a, dev, "init_state", init_state, self._states, t)
+        self._dense(a, dev, "final_state", final_state, self._states, t)
         self._seq(a, dev, seq_start)
         self._call(self._run, a, dev, stream)
 
     def run_backward(self, x, w, dy, dx, dw, dbias=None, bias=None, init_state=None, dinit_state=None, dfinal_state=None,
                      seq_start=None, ws=None, stream=None):
-        (a, dev), C, t, f32 = self._block(x), self._C, self.dtype, self._torch.float32
-        self._rows_of(a, dev, "x", x, self.rows, C)
-        self._rows_of(a, dev, "dy", dy, self.rows, C)
-        self._rows_of(a, dev, "dx", dx, self.rows, C)
-        self._dense(a, dev, "w", w, C * self._W, t)
-        self._dense(a, dev, "dw", dw, C * self._W, f32)
-        self._dense(a, dev, "dbias", dbias, C, f32)
-        self._dense(a, dev, "bias", bias, C, t)
+        (a, dev), C, t, f32, rows = self._block(x), self._C, self.dtype, self._torch.float32, self._row_form
+        self._rows_of(a, dev, "x", x, rows)
+        self._rows_of(a, dev, "dy", dy, rows)
+        self._rows_of(a, dev, "dx", dx, rows)
+        self._dense(a, dev, "w", w, self._taps, t)
+        self._dense(a, dev, "dw", dw, self._taps, f32)
+        self._vector(a, dev, "dbias", dbias, C, f32)
+        self._vector(a, dev, "bias", bias, C, t)
         for name, s in (("init_state", init_state), ("dinit_state", dinit_state), ("dfinal_state", dfinal_state)):
-            self._dense(a, dev, name, s, self._state_numel, t)
+            self._dense(a, dev, name, s, self._states, t)
         self._seq(a, dev, seq_start)
         self._workspace(a, dev, ws, self.workspace_bytes)
         self._call(self._backward_run, a, dev, stream)
@@ -309,11 +374,13 @@ class CausalConvPlan(_SsmPlan):
         """x, y [rows, C]; state [num_slots, W-1, C], updated in place; slots int32 [rows] or None (row i uses state i)."""
         (a, dev), C, t = self._block(x), self._C, self.dtype
         rows, pool = x.numel() // C, state.shape[0]
-        self._rows_of(a, dev, "x", x, rows, C)
-        self._rows_of(a, dev, "y", y, rows, C)
-        self._dense(a, dev, "w", w, C * self._W, t)
-        self._dense(a, dev, "bias", bias, C, t)
-        self._dense(a, dev, "state", state, pool * (self._W - 1) * C, t)
+        row_form, states = self._step_forms.get((rows, pool)) or self._new_step(
+            rows, pool, _Form(rows, C, rows=rows), _Form(pool, self._W - 1, C))
+        self._rows_of(a, dev, "x", x, row_form)
+        self._rows_of(a, dev, "y", y, row_form)
+        self._dense(a, dev, "w", w, self._taps, t)
+        self._vector(a, dev, "bias", bias, C, t)
+        self._dense(a, dev, "state", state, states, t)
         self._slots(a, dev, slots, rows, pool)
         self._call(self._step_run, a, dev, stream)
 
@@ -329,7 +396,9 @@ class ScanPlan(_SsmPlan):
         self._overrides = wgrad_scan_overrides(int(segments), int(segments_backward))
         super().__init__(problem, hip_device)
         p = self._struct
-        self._C, self._GS, self._CS = int(p.C), int(p.G * p.S), int(p.C * p.S)
+        self._C, self._G, self._S = int(p.C), int(p.G), int(p.S)
+        self._row_forms = self._forms(self.rows, *self._lead())
+        self._rates, self._states = _Form(self._C, self._S), _Form(int(p.N), self._C, self._S)
         self.info = wgrad_scan_plan_query(self)
         self.workspace_bytes = self.info["workspace_bytes"]
         self.workspace_bytes_backward = self.info["workspace_bytes_backward"]
@@ -351,24 +420,28 @@ class ScanPlan(_SsmPlan):
         """Buffer for the states that run leaves for run_backward."""
         return self._bytes(self.saved_bytes, device)
 
-    def _inputs(self, rows, x, delta, A, B, C, D, z, delta_bias):
-        (a, dev), n, f32 = self._block(x), self._C, self._torch.float32
-        self._rows_of(a, dev, "x", x, rows, n)
-        self._rows_of(a, dev, "delta", delta, rows, n)
-        self._rows_of(a, dev, "B", B, rows, self._GS)
-        self._rows_of(a, dev, "C", C, rows, self._GS)
+    def _forms(self, rows, *lead):
+        """The forms of rows of channels, and of B and C."""
+        return _Form(*lead, self._C, rows=rows), _Form(*lead, self._G, self._S, rows=rows)
+
+    def _inputs(self, forms, x, delta, A, B, C, D, z, delta_bias):
+        (a, dev), n, f32, (rows, bc) = self._block(x), self._C, self._torch.float32, forms
+        self._rows_of(a, dev, "x", x, rows)
+        self._rows_of(a, dev, "delta", delta, rows)
+        self._rows_of(a, dev, "B", B, bc)
+        self._rows_of(a, dev, "C", C, bc)
         if z is not None:
-            self._rows_of(a, dev, "z", z, rows, n)
-        self._dense(a, dev, "A", A, self._CS, f32)
-        self._dense(a, dev, "D", D, n, f32)
-        self._dense(a, dev, "delta_bias", delta_bias, n, f32)
+            self._rows_of(a, dev, "z", z, rows)
+        self._dense(a, dev, "A", A, self._rates, f32)
+        self._vector(a, dev, "D", D, n, f32)
+        self._vector(a, dev, "delta_bias", delta_bias, n, f32)
         return a, dev
 
     def run(self, x, delta, A, B, C, y, D=None, z=None, delta_bias=None, init_state=None, final_state=None, saved=None,
             seq_start=None, ws=None, stream=None):
-        a, dev = self._inputs(self.rows, x, delta, A, B, C, D, z, delta_bias)
-        self._rows_of(a, dev, "y", y, self.rows, self._C)
-        states, f32 = self._struct.N * self._CS, self._torch.float32
+        a, dev = self._inputs(self._row_forms, x, delta, A, B, C, D, z, delta_bias)
+        self._rows_of(a, dev, "y", y, self._row_forms[0])
+        states, f32 = self._states, self._torch.float32
         self._dense(a, dev, "init_state", init_state, states, f32)
         self._dense(a, dev, "final_state", final_state, states, f32)
         self._seq(a, dev, seq_start)
@@ -380,23 +453,22 @@ class ScanPlan(_SsmPlan):
     def run_backward(self, x, delta, A, B, C, dy, saved, dx, ddelta, dA, dB, dC, D=None, z=None, delta_bias=None, dD=None,
                      dz=None, ddelta_bias=None, dinit_state=None, dfinal_state=None, seq_start=None, ws=None, stream=None):
         """The gradients from the same inputs as run's and the states that it left in saved."""
-        rows, n, f32 = self.rows, self._C, self._torch.float32
-        a, dev = self._inputs(rows, x, delta, A, B, C, D, z, delta_bias)
-        self._rows_of(a, dev, "dy", dy, rows, n)
-        self._rows_of(a, dev, "dx", dx, rows, n)
-        self._rows_of(a, dev, "ddelta", ddelta, rows, n)
+        (rows, bc), n, f32 = self._row_forms, self._C, self._torch.float32
+        a, dev = self._inputs(self._row_forms, x, delta, A, B, C, D, z, delta_bias)
+        self._rows_of(a, dev, "dy", dy, rows)
+        self._rows_of(a, dev, "dx", dx, rows)
+        self._rows_of(a, dev, "ddelta", ddelta, rows)
         if (z is None) != (dz is None):
             raise ValueError("dz belongs to z, and only to it")
         if dz is not None:
-            self._rows_of(a, dev, "dz", dz, rows, n)
-        self._rows_of(a, dev, "dB", dB, rows, self._GS)
-        self._rows_of(a, dev, "dC", dC, rows, self._GS)
-        self._dense(a, dev, "dA", dA, self._CS, f32)
-        self._dense(a, dev, "dD", dD, n, f32)
-        self._dense(a, dev, "ddelta_bias", ddelta_bias, n, f32)
-        states = self._struct.N * self._CS
-        self._dense(a, dev, "dinit_state", dinit_state, states, f32)
-        self._dense(a, dev, "dfinal_state", dfinal_state, states, f32)
+            self._rows_of(a, dev, "dz", dz, rows)
+        self._rows_of(a, dev, "dB", dB, bc)
+        self._rows_of(a, dev, "dC", dC, bc)
+        self._dense(a, dev, "dA", dA, self._rates, f32)
+        self._vector(a, dev, "dD", dD, n, f32)
+        self._vector(a, dev, "ddelta_bias", ddelta_bias, n, f32)
+        self._dense(a, dev, "dinit_state", dinit_state, self._states, f32)
+        self._dense(a, dev, "dfinal_state", dfinal_state, self._states, f32)
         self._seq(a, dev, seq_start)
         self._buffer(a, dev, "saved", saved, self.saved_bytes)
         self._workspace(a, dev, ws, self.workspace_bytes_backward)
@@ -405,9 +477,11 @@ class ScanPlan(_SsmPlan):
     def run_step(self, x, delta, A, B, C, state, y, D=None, z=None, delta_bias=None, slots=None, stream=None):
         """x, delta, z, y [rows, C]; state [num_slots, C, S] fp32, updated in place; slots int32 [rows] or None."""
         rows, pool = x.numel() // self._C, state.shape[0]
-        a, dev = self._inputs(rows, x, delta, A, B, C, D, z, delta_bias)
-        self._rows_of(a, dev, "y", y, rows, self._C)
-        self._dense(a, dev, "state", state, pool * self._CS, self._torch.float32)
+        forms, states = self._step_forms.get((rows, pool)) or self._new_step(
+            rows, pool, self._forms(rows, rows), _Form(pool, self._C, self._S))
+        a, dev = self._inputs(forms, x, delta, A, B, C, D, z, delta_bias)
+        self._rows_of(a, dev, "y", y, forms[0])
+        self._dense(a, dev, "state", state, states, self._torch.float32)
         self._slots(a, dev, slots, rows, pool)
         self._call(self._step_run, a, dev, stream)
 

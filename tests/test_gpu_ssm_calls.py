@@ -53,3 +53,67 @@ def test_single_calls_with_their_own_workspace(how):
     _check_scan({"y": y}, want, scale, "bf16", L, C, T)
     want, scale = _ref_conv(cc, cstarts, "silu", grads=False)
     ref.assert_close("y", u, want["y"], scale["y"], "bf16", 32)
+
+
+def _refused(call, *names):
+    """Every operand in `names`, with its last two axes exchanged (as many elements, another order), is a ValueError that
+    names it; the call itself is none."""
+    base = call.keywords
+    call()
+    for name in names:
+        bad = base[name].transpose(-1, -2).contiguous()
+        assert bad.shape != base[name].shape, name
+        with pytest.raises(ValueError, match=f"^{name}: "):
+            call(**{name: bad})
+    torch.cuda.synchronize()
+
+
+def test_operands_of_another_shape_are_refused():
+    from functools import partial
+    N, L, C, W, G, S = 2, 10, 12, 4, 3, 5
+
+    def t(*shape):
+        return torch.zeros(*shape, device="cuda")
+
+    conv = gcb.CausalConvPlan({"dtype": "fp32", "N": N, "L": L, "C": C, "W": W})
+    rows = {k: t(N, L, C) for k in ("x", "y")}
+    states = {k: t(N, W - 1, C) for k in ("init_state", "final_state")}
+    _refused(partial(conv.run, w=t(C, W), **rows, **states), "x", "y", "w", "init_state", "final_state")
+    rows = {k: t(N, L, C) for k in ("x", "dy", "dx")}
+    states = {k: t(N, W - 1, C) for k in ("init_state", "dinit_state", "dfinal_state")}
+    _refused(partial(conv.run_backward, w=t(C, W), dw=t(C, W), ws=conv.new_workspace(), **rows, **states),
+             "x", "dy", "dx", "w", "dw", "init_state", "dinit_state", "dfinal_state")
+    _refused(partial(conv.run_step, x=t(2, C), w=t(C, W), state=t(7, W - 1, C), y=t(2, C)), "x", "w", "state", "y")
+
+    scan = gcb.ScanPlan({"dtype": "fp32", "N": N, "L": L, "C": C, "G": G, "S": S})
+    ins = {**{k: t(N, L, C) for k in ("x", "delta", "z")}, **{k: t(N, L, G, S) for k in ("B", "C")}, "A": t(C, S)}
+    saved, ws = scan.new_saved(), scan.new_workspace()
+    _refused(partial(scan.run, y=t(N, L, C), init_state=t(N, C, S), final_state=t(N, C, S), saved=saved, ws=ws, **ins),
+             "x", "delta", "z", "B", "C", "A", "y", "init_state", "final_state")
+    outs = {**{k: t(N, L, C) for k in ("dy", "dx", "ddelta", "dz")}, **{k: t(N, L, G, S) for k in ("dB", "dC")}, "dA": t(C, S)}
+    _refused(partial(scan.run_backward, saved=saved, ws=ws, dinit_state=t(N, C, S), dfinal_state=t(N, C, S), **ins, **outs),
+             "x", "delta", "z", "B", "C", "A", "dy", "dx", "ddelta", "dz", "dB", "dC", "dA", "dinit_state", "dfinal_state")
+    one = {**{k: t(4, C) for k in ("x", "delta", "z", "y")}, **{k: t(4, G, S) for k in ("B", "C")}, "A": t(C, S)}
+    _refused(partial(scan.run_step, state=t(6, C, S), **one), "x", "delta", "z", "y", "B", "C", "A", "state")
+
+
+def test_operands_of_merged_and_split_axes():
+    """The same elements in the same order: rows of all sequences in one axis, one more axis of 1, G and S merged."""
+    N, L, C, W, G, S = 2, 10, 12, 4, 3, 5
+    g = torch.Generator().manual_seed(3)
+
+    def t(*shape):
+        return torch.randn(*shape, generator=g).cuda()
+
+    conv = gcb.CausalConvPlan({"dtype": "fp32", "N": N, "L": L, "C": C, "W": W})
+    x, w = t(N, L, C), t(C, W)
+    want, got = torch.zeros_like(x), torch.zeros_like(x)
+    conv.run(x, w, want)
+    conv.run(x.view(N * L, C), w.view(C, 1, W), got.view(1, N * L, C))
+    assert torch.equal(got, want) and bool(want.any())
+    scan = gcb.ScanPlan({"dtype": "fp32", "N": N, "L": L, "C": C, "G": G, "S": S})
+    A, b, c = -t(C, S).abs(), t(N, L, G, S), t(N, L, G, S)
+    scan.run(x, x, A, b, c, want, ws=scan.new_workspace())
+    scan.run(x.view(-1, C), x, A, b.view(N * L, G * S), c.view(N * L, G, S), got, ws=scan.new_workspace())
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and bool(want.any())
