@@ -61,9 +61,10 @@ struct Rows {
 // A lane's channels. VEC (C >= E): the last lane's are moved back until they
 // end with the row, so that every lane has E of them; the ones it shares with
 // the lane before it are computed, and written, the same twice. Vector accesses
-// need no more than the element's alignment here (the unaligned access mode
-// that this platform runs in): an odd row stride costs a few percent, not the
-// vector. Only rows shorter than a vector are accessed by single elements.
+// need no more than the element's alignment here: they go through buffer
+// descriptors, in the unaligned access mode that this platform runs in (through
+// pointers the compiler may assume a vector's alignment), and an odd row stride
+// costs a few percent, not the vector. Only rows shorter than a vector are accessed by single elements.
 template <int E, bool VEC>
 struct Lane {
     int c, nv;
@@ -144,11 +145,12 @@ __global__ __launch_bounds__(256) void cconv_kernel(const CconvArgs a) {
     }
     // the run that ends the sequence leaves its last W - 1 inputs
     if (a.final_state && pc.last && (end == pc.len) && (first < end || (pc.len == 0 && slot == 0))) {
+        const auto rf = tile_rsrc<T>(a.final_state, (int64_t)pc.n * (W - 1), a.C);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             Pack<T, E> v;
             rows.window(v, pc.len - (W - 1) + j);
-            v.store(static_cast<T*>(a.final_state) + ((int64_t)pc.n * (W - 1) + j) * a.C + c, VEC, nv);
+            v.store(rf, row_offset(j, 0, rows.C, rows.c), VEC, nv);
         }
     }
 }
@@ -237,7 +239,7 @@ __global__ __launch_bounds__(256) void cconv_bwd_kernel(const CconvArgs a) {
             if (r < 0 && starts) inner(r + W - 1, dx);
             if (r >= fin) {
                 Pack<T, E> v;
-                v.load(static_cast<const T*>(a.dfinal) + ((int64_t)pc.n * (W - 1) + r - fin) * a.C + c, VEC, nv);
+                v.load(tile_rsrc<T>(a.dfinal, (int64_t)pc.n * (W - 1), a.C), row_offset(r, fin, rows.C, rows.c), VEC, nv);
 #pragma unroll
                 for (int i = 0; i < E; ++i) dx[i] += v.get(i);
             }
@@ -246,7 +248,7 @@ __global__ __launch_bounds__(256) void cconv_bwd_kernel(const CconvArgs a) {
             for (int i = 0; i < E; ++i) out.set(i, dx[i]);
             out.store(rdx, rows.at(r, sdx), VEC, r >= first && r < end ? nv : 0);
             if (r < 0 && starts && a.dinit)
-                out.store(static_cast<T*>(a.dinit) + ((int64_t)pc.n * (W - 1) + (W - 1) + r) * a.C + c, VEC, nv);
+                out.store(tile_rsrc<T>(a.dinit, (int64_t)pc.n * (W - 1), a.C), row_offset(r, 1 - W, rows.C, rows.c), VEC, nv);
         };
         // whole batches of the run's own rows
         int t = first;

@@ -62,8 +62,9 @@ struct Pack {
                 w[i >> 1] = h;
         }
     }
-    // vec: p is aligned to the pack (at most 16 bytes; 8 where the pack is an
-    // odd number of 8-byte halves) and nv is E or <= 0;
+    // Through a pointer, as the kernels for single tokens do, which choose by
+    // alignment. vec: p is aligned to the pack (at most 16 bytes; 8 where the
+    // pack is an odd number of 8-byte halves) and nv is E or <= 0;
     // otherwise elements from nv on are not touched (loaded as zeros)
     __device__ __forceinline__ void load(const T* p, bool vec, int nv) {
         zero();
@@ -92,9 +93,11 @@ struct Pack {
                 if (i < nv) put_bits(i, p + i);
         }
     }
-    // The same through a buffer descriptor, without a branch: off is the byte
-    // offset of element 0, accesses of elements from nv on are sent out of the
-    // buffer's range (loads give 0, stores are dropped).
+    // The same through a buffer descriptor, as the kernels for whole sequences
+    // do, without a branch and at any alignment of the elements (the unaligned
+    // access mode): off is the byte offset of element 0, accesses of elements
+    // from nv on are sent out of the buffer's range (loads give 0, stores are
+    // dropped).
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off, bool vec, int nv) {
         if (vec) {
             off = nv > 0 ? off : dev::kBufOob;

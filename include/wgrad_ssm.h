@@ -18,12 +18,13 @@
  *     of 0 are allowed. The array is read on the device only: a value out of
  *     range cannot make a kernel leave its buffers (starts and ends are
  *     clamped to 0..T and the length to L) but gives meaningless results.
- * Pointers need the alignment of their element type; kernels use 16-byte
- * accesses where pointers, row strides and channel counts allow them. Row
- * strides are at least the row's width and at most 2^23 elements (of a
- * convolution 2^20). Outputs
- * must not overlap inputs or each other, except where an entry point updates
- * a state in place.
+ * Pointers need the alignment of their element type, workspaces and saved
+ * states 16 bytes. Runs over sequences use accesses of up to 16 bytes at any
+ * such alignment; the runs for single tokens use them where pointers, row
+ * strides and channels come in whole ones. Row strides are at least the row's
+ * width and at most 2^23 elements (of a convolution 2^20). Outputs must not
+ * overlap inputs or each other, except where an entry point updates a state in
+ * place.
  */
 #ifndef WGRAD_SSM_H
 #define WGRAD_SSM_H

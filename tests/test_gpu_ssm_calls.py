@@ -117,3 +117,34 @@ def test_operands_of_merged_and_split_axes():
     scan.run(x.view(-1, C), x, A, b.view(N * L, G * S), c.view(N * L, G, S), got, ws=scan.new_workspace())
     torch.cuda.synchronize()
     assert torch.equal(got, want) and bool(want.any())
+
+
+@pytest.mark.parametrize("dtype,C", [("bf16", 40), ("fp16", 33), ("fp32", 6), ("bf16", 5)])
+def test_operands_that_lie_on_an_element_only(dtype, C):
+    """Every operand of the convolution, its states too, one element past a vector's alignment."""
+    N, L, W = 3, 37, 4
+    c, p, starts, T = _conv_case(dtype, C, W, N, L, None, "silu", True, 0)
+    want, scale = _ref_conv(c, starts, "silu")
+
+    def off(t, kind=dtype):
+        whole = torch.full((t.numel() + 9,), float("nan"), dtype=ref.TORCH[kind], device="cuda")
+        inner = whole[1:1 + t.numel()].view(t.shape)
+        inner.copy_(t.cuda())
+        return whole, inner
+
+    ins = {k: off(v)[1] for k, v in c.items()}
+    outs = {k: off(torch.full(s, float("nan"))) for k, s in
+            {"y": (T, C), "final_state": (N, W - 1, C), "dx": (T, C), "dinit_state": (N, W - 1, C)}.items()}
+    sums = {k: off(torch.full(s, float("nan")), "fp32") for k, s in {"dw": (C, W), "dbias": (C,)}.items()}
+    plan = gcb.CausalConvPlan(p)
+    print(f"[gpu] conv {p}", flush=True)
+    plan.run(ins["x"], ins["w"], outs["y"][1], bias=ins["bias"], init_state=ins["init"], final_state=outs["final_state"][1])
+    plan.run_backward(ins["x"], ins["w"], ins["dy"], outs["dx"][1], sums["dw"][1], dbias=sums["dbias"][1], bias=ins["bias"],
+                      init_state=ins["init"], dinit_state=outs["dinit_state"][1], dfinal_state=ins["dfinal"], ws=plan.new_workspace())
+    torch.cuda.synchronize()
+    for k, (whole, inner) in {**outs, **sums}.items():
+        assert bool(torch.isnan(whole[:1]).all()) and bool(torch.isnan(whole[1 + inner.numel():]).all()), k
+        if k == "final_state":
+            assert torch.equal(inner.double().cpu(), want[k])
+        else:
+            ref.assert_close(k, inner, want[k], scale[k], "fp32" if k in sums else dtype, 2 * W + 24 + (T if k in sums else 0))
