@@ -36,14 +36,22 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t elem_bytes(int dtype) { return dtype == WGRAD_FP32 ? 4 : 2; }
 
 // No exception leaves a C entry point: a host allocation that fails inside
-// one (a reason string, a plan) ends as an error code.
+// one (a reason string, a plan) ends as an error code, with the reason if
+// there is memory for that.
+int out_of_memory() noexcept {
+    try {
+        return invalid("out of host memory");
+    } catch (...) {
+        return WGRAD_ERR_INVALID_ARG;
+    }
+}
 template <class F>
 int guarded(F f) {
     try {
         wgrad::clear_error();
         return f();
     } catch (...) {
-        return WGRAD_ERR_INVALID_ARG;
+        return out_of_memory();
     }
 }
 
