@@ -92,8 +92,8 @@ __device__ __forceinline__ void load_params(const CconvArgs& a, int c, int nv, f
 // a large copy's rate.
 template <class T, int E, int W, bool VEC, bool SILU>
 __global__ __launch_bounds__(256) void cconv_kernel(const CconvArgs a) {
-    const int wg = workgroup(), id = wg / a.cblks, cb = wg - id * a.cblks;
-    if (id >= a.pc.count) return;
+    const uint32_t wg = a.first + blockIdx.x;
+    const int id = wg / a.cblks, cb = wg - id * a.cblks;
     const Piece pc = find_piece(a.pc, id);
     if (pc.rows <= 0 && !pc.last) return;
     const int cl = a.cl, lane = threadIdx.x & (cl - 1), slot = threadIdx.x / cl;
@@ -164,8 +164,8 @@ __global__ __launch_bounds__(256) void cconv_kernel(const CconvArgs a) {
 // element under them.
 template <class T, int E, int W, bool VEC, bool SILU>
 __global__ __launch_bounds__(256) void cconv_bwd_kernel(const CconvArgs a) {
-    const int wg = workgroup(), id = wg / a.cblks, cb = wg - id * a.cblks;
-    if (id >= a.pc.count) return;
+    const uint32_t wg = a.first + blockIdx.x;
+    const int id = wg / a.cblks, cb = wg - id * a.cblks;
     const Piece pc = find_piece(a.pc, id);
     const int cl = a.cl, lane = threadIdx.x & (cl - 1), slot = threadIdx.x / cl;
     const Lane<E, VEC> ln(a, (cb * cl + lane) * E);
@@ -351,7 +351,7 @@ __global__ __launch_bounds__(256) void cconv_reduce_kernel(const CconvReduceArgs
 template <class T, int E, int W>
 __global__ __launch_bounds__(256) void cconv_step_kernel(const CconvStepArgs a) {
     const int cv = (a.C + E - 1) / E;
-    const int64_t idx = (int64_t)workgroup() * 256 + threadIdx.x;
+    const int64_t idx = (int64_t)(a.first + blockIdx.x) * 256 + threadIdx.x;
     const int64_t row = idx / cv;
     if (row >= a.rows) return;
     const int c = (int)(idx - row * cv) * E;
@@ -411,16 +411,19 @@ int launch_cconv(int dtype, const CconvArgs& a, void* stream) {
         return by_taps(a.W, [&](auto w) {
             constexpr int E = 16 / sizeof(T);
             constexpr int W = decltype(w)::value;
-            const dim3 grid = launch_grid((int64_t)a.pc.count * a.cblks);
             const hipStream_t s = static_cast<hipStream_t>(stream);
-            if (a.vec && a.silu)
-                cconv_kernel<T, E, W, true, true><<<grid, 256, 0, s>>>(a);
-            else if (a.vec)
-                cconv_kernel<T, E, W, true, false><<<grid, 256, 0, s>>>(a);
-            else if (a.silu)
-                cconv_kernel<T, E, W, false, true><<<grid, 256, 0, s>>>(a);
-            else
-                cconv_kernel<T, E, W, false, false><<<grid, 256, 0, s>>>(a);
+            CconvArgs v = a;
+            for_launches((int64_t)a.pc.count * a.cblks, [&](uint32_t first, uint32_t grid) {
+                v.first = first;
+                if (a.vec && a.silu)
+                    cconv_kernel<T, E, W, true, true><<<grid, 256, 0, s>>>(v);
+                else if (a.vec)
+                    cconv_kernel<T, E, W, true, false><<<grid, 256, 0, s>>>(v);
+                else if (a.silu)
+                    cconv_kernel<T, E, W, false, true><<<grid, 256, 0, s>>>(v);
+                else
+                    cconv_kernel<T, E, W, false, false><<<grid, 256, 0, s>>>(v);
+            });
             return (int)hipGetLastError();
         });
     });
@@ -431,16 +434,19 @@ int launch_cconv_bwd(int dtype, const CconvArgs& a, void* stream) {
         using T = decltype(t);
         return by_taps(a.W, [&](auto w) {
             constexpr int E = kConvBwdVec, W = decltype(w)::value;
-            const dim3 grid = launch_grid((int64_t)a.pc.count * a.cblks);
             const hipStream_t s = static_cast<hipStream_t>(stream);
-            if (a.vec && a.silu)
-                cconv_bwd_kernel<T, E, W, true, true><<<grid, 256, 0, s>>>(a);
-            else if (a.vec)
-                cconv_bwd_kernel<T, E, W, true, false><<<grid, 256, 0, s>>>(a);
-            else if (a.silu)
-                cconv_bwd_kernel<T, E, W, false, true><<<grid, 256, 0, s>>>(a);
-            else
-                cconv_bwd_kernel<T, E, W, false, false><<<grid, 256, 0, s>>>(a);
+            CconvArgs v = a;
+            for_launches((int64_t)a.pc.count * a.cblks, [&](uint32_t first, uint32_t grid) {
+                v.first = first;
+                if (a.vec && a.silu)
+                    cconv_bwd_kernel<T, E, W, true, true><<<grid, 256, 0, s>>>(v);
+                else if (a.vec)
+                    cconv_bwd_kernel<T, E, W, true, false><<<grid, 256, 0, s>>>(v);
+                else if (a.silu)
+                    cconv_bwd_kernel<T, E, W, false, true><<<grid, 256, 0, s>>>(v);
+                else
+                    cconv_bwd_kernel<T, E, W, false, false><<<grid, 256, 0, s>>>(v);
+            });
             return (int)hipGetLastError();
         });
     });
@@ -458,8 +464,11 @@ int launch_cconv_step(int dtype, const CconvStepArgs& a, void* stream) {
         return by_taps(a.W, [&](auto w) {
             constexpr int E = 16 / sizeof(T);
             const int64_t threads = a.rows * ((a.C + E - 1) / E);
-            cconv_step_kernel<T, E, decltype(w)::value>
-                <<<launch_grid((threads + 255) / 256), 256, 0, static_cast<hipStream_t>(stream)>>>(a);
+            CconvStepArgs v = a;
+            for_launches((threads + 255) / 256, [&](uint32_t first, uint32_t grid) {
+                v.first = first;
+                cconv_step_kernel<T, E, decltype(w)::value><<<grid, 256, 0, static_cast<hipStream_t>(stream)>>>(v);
+            });
             return (int)hipGetLastError();
         });
     });

@@ -258,8 +258,8 @@ __global__ __launch_bounds__(256) void fwd_kernel(const ScanArgs a) {
     __shared__ __attribute__((aligned(16))) float sC[TT][SP];
 
     const int nblk = a.cblks_g * a.G;
-    const int group = workgroup(), id = group / nblk;
-    if (id >= a.pc.count) return;
+    const uint32_t group = a.first + blockIdx.x;
+    const int id = group / nblk;
     const Block cb = channel_block<scan_unit(LPC)>(a, group - id * nblk);
     const Piece pc = find_piece(a.pc, id);
     if (SUM ? (pc.rows <= 0 || pc.last) : (pc.rows <= 0 && !pc.last)) return;
@@ -429,8 +429,8 @@ __global__ __launch_bounds__(256) void bwd_sum_kernel(const ScanArgs a) {
     __shared__ __attribute__((aligned(16))) float sC[TT][SP];
 
     const int nblk = a.cblks_g * a.G;
-    const int group = workgroup(), id = group / nblk;
-    if (id >= a.pc.count) return;
+    const uint32_t group = a.first + blockIdx.x;
+    const int id = group / nblk;
     const Block cb = channel_block<scan_unit(LPC)>(a, group - id * nblk);
     const Piece pc = find_piece(a.pc, id);
     if (pc.rows <= 0 || pc.j == 0) return;
@@ -603,8 +603,8 @@ __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(co
     __shared__ float sSum[2 * E][256];
 
     const int nblk = a.cblks_g * a.G;
-    const int group = workgroup(), id = group / nblk;
-    if (id >= a.pc.count) return;
+    const uint32_t group = a.first + blockIdx.x;
+    const int id = group / nblk;
     const Block cb = channel_block<scan_unit(LPC)>(a, group - id * nblk);
     const Piece pc = find_piece(a.pc, id);
     const int rows = max(pc.rows, 0);
@@ -895,22 +895,30 @@ __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(co
     }
 }
 
-template <class T, int NS, int LPC, int VEC>
-int run_fwd(const ScanArgs& a, hipStream_t s) {
-    const dim3 grid = launch_grid((int64_t)a.pc.count * a.cblks_g * a.G);
-    if (a.split) fwd_kernel<T, NS, LPC, VEC, true><<<grid, 256, 0, s>>>(a);
-    fwd_kernel<T, NS, LPC, VEC, false><<<grid, 256, 0, s>>>(a);
+// The sums of all segments go out before the kernels that fold them.
+template <class F>
+int launch_all(const ScanArgs& a, F launch) {
+    ScanArgs v = a;
+    for_launches((int64_t)a.pc.count * a.cblks_g * a.G, [&](uint32_t first, uint32_t grid) {
+        v.first = first;
+        launch(grid, v);
+    });
     return (int)hipGetLastError();
 }
 template <class T, int NS, int LPC, int VEC>
+int run_fwd(const ScanArgs& a, hipStream_t s) {
+    if (a.split) launch_all(a, [&](uint32_t grid, const ScanArgs& v) { fwd_kernel<T, NS, LPC, VEC, true><<<grid, 256, 0, s>>>(v); });
+    return launch_all(a, [&](uint32_t grid, const ScanArgs& v) { fwd_kernel<T, NS, LPC, VEC, false><<<grid, 256, 0, s>>>(v); });
+}
+template <class T, int NS, int LPC, int VEC>
 int run_bwd(const ScanArgs& a, hipStream_t s) {
-    const dim3 grid = launch_grid((int64_t)a.pc.count * a.cblks_g * a.G);
-    if (a.split) bwd_sum_kernel<T, NS, LPC, VEC><<<grid, 256, 0, s>>>(a);
-    if (a.z)
-        bwd_kernel<T, NS, LPC, VEC, true><<<grid, 256, 0, s>>>(a);
-    else
-        bwd_kernel<T, NS, LPC, VEC, false><<<grid, 256, 0, s>>>(a);
-    return (int)hipGetLastError();
+    if (a.split) launch_all(a, [&](uint32_t grid, const ScanArgs& v) { bwd_sum_kernel<T, NS, LPC, VEC><<<grid, 256, 0, s>>>(v); });
+    return launch_all(a, [&](uint32_t grid, const ScanArgs& v) {
+        if (a.z)
+            bwd_kernel<T, NS, LPC, VEC, true><<<grid, 256, 0, s>>>(v);
+        else
+            bwd_kernel<T, NS, LPC, VEC, false><<<grid, 256, 0, s>>>(v);
+    });
 }
 
 template <class T, int NS, int LPC>

@@ -17,7 +17,7 @@ using scan::f32x4;
 // 16 states, 64 channel blocks: 13.9 us for 70 MB, which the caches hold).
 template <class T>
 __global__ __launch_bounds__(256) void scan_reduce_kernel(const ScanReduceArgs a, int64_t n_bc, int64_t n_a) {
-    int64_t i = (int64_t)workgroup() * 256 + threadIdx.x;
+    int64_t i = (int64_t)(a.first + blockIdx.x) * 256 + threadIdx.x;
     const int W = 2 * a.SP;
     if (i < n_bc) {
         const int s2 = (int)(i % W);
@@ -55,7 +55,11 @@ template <class T>
 int reduce(const ScanReduceArgs& a, void* stream) {
     const int64_t n_bc = (int64_t)a.rows * a.G * 2 * a.SP, n_a = (int64_t)a.channels * a.SP;
     const int64_t blocks = (n_bc + n_a + 2 * (int64_t)a.channels + 255) / 256;
-    scan_reduce_kernel<T><<<launch_grid(blocks), 256, 0, static_cast<hipStream_t>(stream)>>>(a, n_bc, n_a);
+    ScanReduceArgs v = a;
+    for_launches(blocks, [&](uint32_t first, uint32_t grid) {
+        v.first = first;
+        scan_reduce_kernel<T><<<grid, 256, 0, static_cast<hipStream_t>(stream)>>>(v, n_bc, n_a);
+    });
     return (int)hipGetLastError();
 }
 
@@ -68,9 +72,9 @@ template <class T, int NS, int LPC>
 __global__ __launch_bounds__(256) void scan_step_kernel(const ScanStepArgs a) {
     constexpr int CT = 256 / LPC;
     const int cblks = (a.channels + CT - 1) / CT;
-    const int wg = workgroup(), cb = wg % cblks;
+    const uint32_t wg = a.first + blockIdx.x;
     const int64_t row = wg / cblks;
-    if (row >= a.rows) return;
+    const int cb = (int)(wg - row * cblks);
     const int q = threadIdx.x % LPC, s0 = q * NS;
     const int c = cb * CT + (int)threadIdx.x / LPC;
     const bool ok = c < a.channels;
@@ -131,7 +135,11 @@ template <class T, int NS, int LPC>
 int step(const ScanStepArgs& a, hipStream_t s) {
     constexpr int CT = 256 / LPC;
     const int64_t blocks = a.rows * ((a.channels + CT - 1) / CT);
-    scan_step_kernel<T, NS, LPC><<<launch_grid(blocks), 256, 0, s>>>(a);
+    ScanStepArgs v = a;
+    for_launches(blocks, [&](uint32_t first, uint32_t grid) {
+        v.first = first;
+        scan_step_kernel<T, NS, LPC><<<grid, 256, 0, s>>>(v);
+    });
     return (int)hipGetLastError();
 }
 template <class T>

@@ -13,13 +13,6 @@ using dev::lds_barrier;
 using dev::u32x2;
 using dev::u32x4;
 
-// The number of a workgroup in a grid of grid_of() (below 2^31).
-__device__ __forceinline__ int workgroup() { return (int)(blockIdx.y * (uint32_t)kGridRow + blockIdx.x); }
-inline dim3 launch_grid(int64_t workgroups) {
-    const Grid g = grid_of(workgroups);
-    return dim3(g.x, g.y);
-}
-
 struct Bf16 { uint16_t b; };
 struct Fp16 { uint16_t b; };
 struct Fp32 { float f; };

@@ -45,13 +45,18 @@ constexpr PieceRows piece_rows(int32_t j, int32_t len, int32_t rows) {
     return {t0, left < rows ? left : rows, some && (j == 0 ? len <= rows : left > 0 && left <= rows)};
 }
 
-// The grid of a launch. Work items along one axis have to stay below 2^32 (a
-// larger grid is cut off without an error), so workgroups of 256 beyond 2^20
-// lie in rows of 2^20; those of the last row that are too many leave at once.
-constexpr int64_t kGridRow = int64_t(1) << 20;
-struct Grid { uint32_t x, y; };
-constexpr Grid grid_of(int64_t workgroups) {
-    return {(uint32_t)(workgroups < kGridRow ? workgroups : kGridRow), (uint32_t)((workgroups + kGridRow - 1) / kGridRow)};
+// Workgroups of 256 in one launch at most. Work items along an axis have to stay
+// below 2^32, and a larger grid is cut off without an error, so that more of
+// them go out as several launches, each with the number of its first workgroup.
+// (As rows of a second axis, whose last is too long, every kernel would have to
+// look whether its workgroup is one too many: single tokens, 256 rows of 4096
+// channels, 30.5 us against 28.8.)
+constexpr int64_t kLaunchGroups = int64_t(1) << 23;
+// Calls launch(first, count) for them.
+template <class F>
+constexpr void for_launches(int64_t workgroups, F launch) {
+    for (int64_t first = 0; first < workgroups; first += kLaunchGroups)
+        launch((uint32_t)first, (uint32_t)(workgroups - first < kLaunchGroups ? workgroups - first : kLaunchGroups));
 }
 
 // The byte offset, from row `base` of a tensor on, of place `at` in row t. For
@@ -72,6 +77,7 @@ struct CconvArgs {
     int32_t cl;                 // lanes of a workgroup along the channels (a power of two <= 256); 256 / cl runs of rows
     int32_t cblks;              // ceil(C / (cl * channels per lane))
     int32_t run;                // rows a lane walks; rows of a piece = run * 256 / cl
+    uint32_t first;             // number of a launch's first workgroup (for_launches)
 };
 
 struct CconvReduceArgs {
@@ -86,6 +92,7 @@ struct CconvStepArgs {
     const int32_t* slots;
     int64_t sx, sy, rows, num_slots;
     int32_t C, W, silu, vec;
+    uint32_t first;
 };
 
 struct ScanArgs {
@@ -103,6 +110,7 @@ struct ScanArgs {
     int32_t units, units_more;  // units of scan_unit() channels per block; the first units_more blocks have one more
     int32_t vec_c, vec_s;       // vector accesses along the channels (see lane_channel), and of four states of B and C
     int32_t split;              // sequences have more than one segment
+    uint32_t first;             // number of a launch's first workgroup (for_launches)
 };
 
 struct ScanReduceArgs {
@@ -111,6 +119,7 @@ struct ScanReduceArgs {
     float *dA, *dD, *ddelta_bias;   // dD, ddelta_bias may be NULL
     int64_t sdB, sdC;
     int32_t rows, channels, G, S, SP, cblks_g, pieces;
+    uint32_t first;
 };
 
 struct ScanStepArgs {
@@ -121,6 +130,7 @@ struct ScanStepArgs {
     const int32_t* slots;
     int64_t sx, sdelta, sB, sC, sz, sy, rows, num_slots;
     int32_t channels, Cg, S, softplus, vec;
+    uint32_t first;
 };
 
 // Rows between two saved states: the backward kernel keeps the decays and

@@ -3,7 +3,7 @@
 // UndefinedBehaviorSanitizer, which ends the program at the first overflow;
 // the sums here are 64-bit. Likewise the offsets of rows in a piece of the
 // convolution (row_offset), which its kernels also form for rows far outside
-// it, and the grids of launches (grid_of). Prints the number of combinations looked at.
+// it, and the launches of large grids (for_launches). Prints the number of combinations looked at.
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -57,12 +57,14 @@ int main() {
                 if (d >= 0 && d <= 263) expect((int64_t)got == want && want < (1LL << 31), "offset of a near row", t, base, row_bytes, 40, 0, 0);
             }
     constexpr int64_t most = (1LL << 31) - 1;                        // workgroups that a plan accepts
-    for (int64_t n : std::initializer_list<int64_t>{1, 255, kGridRow - 1, kGridRow, kGridRow + 1, 3 * kGridRow, (1 << 24) - 1, 1 << 24,
+    for (int64_t n : std::initializer_list<int64_t>{0, 1, 255, kLaunchGroups - 1, kLaunchGroups, kLaunchGroups + 1, (1 << 24) - 1, 1 << 24,
                                                     (1 << 24) + 3, big + 1, most}) {
-        const Grid g = grid_of(n);
-        const int64_t have = (int64_t)g.x * g.y;
-        const bool fits = (int64_t)g.x * 256 < (1LL << 32) && g.y < 65536 && have <= (1LL << 31) && (g.y == 1 || g.x == kGridRow);
-        expect(fits && have >= n && have - n < kGridRow, "grid", (int32_t)n, 0, 0, 0, 0, 0);
+        int64_t next = 0;                                             // each workgroup once, in order
+        for_launches(n, [&](uint32_t first, uint32_t count) {
+            expect((int64_t)first == next && count > 0 && (int64_t)count * 256 < (1LL << 32), "launch", (int32_t)n, 0, 0, 0, 0, 0);
+            next += count;
+        });
+        expect(next == n, "launches", (int32_t)n, 0, 0, 0, 0, 0);
     }
     std::printf("%lld\n", g_seen);
     return 0;
