@@ -85,8 +85,8 @@ __device__ __forceinline__ Block channel_block(const ScanArgs& a, int blk) {
 // stored, the same twice. Vector accesses need no more than the element's
 // alignment (the unaligned access mode that this platform runs in); 2 is an
 // instance of its own because it can write two channels to LDS at once and
-// clamps nothing (bf16, 16 states, 8 x 2048 rows: 326 us forward and 881
-// backward with 4096 channels, 358 and 939 with 4095).
+// clamps nothing (bf16, 16 states, 8 x 2048 rows: 319 us forward and 856
+// backward with 4096 channels, 361 and 905 with 4095).
 template <int E, int VEC>
 __device__ __forceinline__ int lane_channel(int at, int in) {
     return VEC == 1 && at < in ? min(at, in - E) : at;
@@ -239,11 +239,11 @@ __device__ __forceinline__ float deal_sum(const float (&v)[LPC], int q) {
 }
 
 // Forward. SUM: the segment's state from zero and its sum of d only.
-// bf16, 16 states, 8 x 2048 rows of 4096 channels: 322 us, half the rate that
+// bf16, 16 states, 8 x 2048 rows of 4096 channels: 319 us, half the rate that
 // the instructions alone allow. The rest is the staging of a tile (a quarter of
 // a workgroup's cycles: softplus, conversions, LDS writes), its loads and
 // stores, and two or three waves a SIMD to cover them. As segments of one
-// sequence, 1 x 16384 x 4096: 440 us, two fifths of them for the sums.
+// sequence, 1 x 16384 x 4096: 437 us, two fifths of them for the sums.
 // Tiles of 32 rows (16 with 128 channels) cost two barriers each and leave room
 // for five workgroups a CU.
 template <class T, int NS, int LPC, int VEC, bool SUM>
@@ -576,12 +576,20 @@ struct ChannelSum {
 // as they go, about two instructions per value; the waves' shares are joined
 // in LDS and leave one partial per channel block, which the reduce kernel adds
 // in one order. GATE: z is there, so y is needed again for dz.
-// bf16, 16 states, gated, 8 x 2048 rows of 4096 channels: 874 us. Of a chunk's
+// bf16, 16 states, gated, 8 x 2048 rows of 4096 channels: 855 us. Of a chunk's
 // cycles the forward run takes 24 %, the run back with its sums 42, staging 14,
 // loads 10, stores 6, the rest 4: bound by instructions, at two waves a SIMD,
 // since decays and states fill the registers. Chunks of 8 rows, with room for
 // more waves, were slower (1046 us against 946 at the time) and doubled what
-// forward saves. The saved states cost forward 2 %.
+// forward saves. The saved states cost forward 3 %.
+// The launch bound: four states a lane fit the 256 registers that two waves a
+// SIMD leave each, some with scratch (17 to 32 states without a gate, 44 to 60
+// bytes a lane; fp32 with 16 states and a gate, 8 or 16). Eight states a lane
+// (S > 32) do not fit and run one wave a SIMD, with 150 to 205 AGPRs beyond
+// them. So do two lanes a channel (S <= 8): up to 142 AGPRs, and with a gate the
+// LDS of 128 channels, 101 (bf16) or 105 KB (fp32), has room for one workgroup.
+// 4 x 2048 x 4096 bf16, us: 8 states 481, 16 states 510, 64 states 2213, 128
+// states 4751.
 template <class T, int NS, int LPC, int VEC, bool GATE>
 __global__ __launch_bounds__(256, NS == 4 && LPC > 2 ? 2 : 1) void bwd_kernel(const ScanArgs a) {
     using F = Form<T, NS, LPC>;

@@ -13,8 +13,8 @@ using scan::f32x4;
 // Three jobs side by side in one launch, each summing partials in one order:
 // dB and dC over the channel blocks of a group, dA over the pieces, dD and
 // ddelta_bias over the pieces. Consecutive lanes read consecutive words, 16
-// loads at a time, which do not wait for the sum (8192 rows,
-// 16 states, 64 channel blocks: 13.9 us for 70 MB, which the caches hold).
+// loads at a time, which do not wait for the sum (8192 rows, 16 states, 64
+// channel blocks: 14.2 us for 70 MB, which the caches hold).
 template <class T>
 __global__ __launch_bounds__(256) void scan_reduce_kernel(const ScanReduceArgs a, int64_t n_bc, int64_t n_a) {
     int64_t i = (int64_t)(a.first + blockIdx.x) * 256 + threadIdx.x;
@@ -66,7 +66,7 @@ int reduce(const ScanReduceArgs& a, void* stream) {
 // One token per row. A lane takes NS states of a channel through one step;
 // LPC adjacent lanes share the channel and its sum. Bound by reading and
 // writing the states, 8 bytes each: 16-byte accesses, adjacent over the wave
-// (256 rows of 4096 channels, 16 states: 29.3 us for 143 MB, 4.9 TB/s, a large
+// (256 rows of 4096 channels, 16 states: 28.8 us for 143 MB, 5.0 TB/s, a large
 // copy's rate; one row: 3.4 us, the launch and two trips to memory).
 template <class T, int NS, int LPC>
 __global__ __launch_bounds__(256) void scan_step_kernel(const ScanStepArgs a) {

@@ -150,9 +150,9 @@ int conv_shape(CconvArgs& a, const wgrad_cconv_problem& p, int64_t T, int vec, i
     a.C = (int32_t)p.C, a.W = p.W, a.silu = p.activation == WGRAD_ACT_SILU;
     // Long runs re-read fewer rows between runs and leave fewer partial sums;
     // short ones fill the card when there are few rows. Runs of 4 | 16 | 32 rows,
-    // bf16, W = 4, us: forward 1 x 512 x 1024 10.1 | 12.0 | 15.7, 4 x 2048 x 4096
-    // 32.2 | 27.8 | 27.9; backward 1 x 512 x 1024 18.7 | 21.2 | 26.0, 1 x 2048 x
-    // 4096 40.4 | 27.7 | 27.8, 4 x 2048 x 4096 110 | 57.8 | 51.9.
+    // bf16, W = 4, us in a graph: forward 1 x 512 x 1024 4.1 | 6.9 | 10.5, 4 x 2048
+    // x 4096 28.3 | 23.9 | 23.7; backward 1 x 512 x 1024 11.8 | 15.3 | 20.5, 1 x
+    // 2048 x 4096 34.9 | 22.0 | 23.0, 4 x 2048 x 4096 104 | 54.8 | 47.5.
     int run = 4;
     while (run < run_most && T * cv / (2 * run) >= lanes_wanted) run *= 2;
     while (run * (256 / cl) > kConvPieceRows) run /= 2;
@@ -185,14 +185,14 @@ int build_cconv(const wgrad_cconv_problem& p, CconvPlan& out) {
 // whole sequences make enough workgroups of four waves, `enough`. A split
 // computes the decays once more (forward; backward about a quarter more work)
 // and wins it back by filling the card: eight workgroups a CU in all, in steps
-// of kSegmentRows. Measured (bf16, 16 states, us whole -> split, forward and
-// backward): 64 workgroups of 2048 rows 230 -> 79, 600 -> 163; 256 of 2048 rows
-// 230 -> 222, 616 -> 518; 384 of 1024 rows 164 -> 173, 436 -> 404; 512 of 2048
-// rows 322 -> 398, 874 -> 988.
+// of kSegmentRows. Measured (bf16, 16 states, us whole -> split, forward with
+// saved states and backward): 64 workgroups of 2048 rows 225 -> 74, 578 -> 154;
+// 256 of 2048 rows 227 -> 219, 593 -> 510; 384 of 1024 rows 162 -> 178, 423 ->
+// 414; 512 of 2048 rows 319 -> 411, 856 -> 975.
 // A segment also folds the sums of all segments before it, one after another,
 // so no more than about sqrt(L) segments pay: 1 x 16384 rows of 128 channels
-// take 57 + 94 us in 128 segments, 98 + 148 in 512; 1 x 65536 rows 113 + 192 in
-// 256, 250 + 459 in 1024.
+// take 50 + 81 us in 128 segments, 97 + 136 in 512; 1 x 65536 rows 106 + 184 in
+// 256, 296 + 442 in 1024.
 int64_t choose_segment_rows(int64_t T, int64_t L, int64_t nblk, int64_t cus, int64_t enough) {
     if (L == 0 || ceil_div(T, L) * nblk >= enough) return L;   // T / L: packed sequences may be mostly short
     const int64_t least = std::max(ceil_div(T * nblk, 8 * cus), (int64_t)std::sqrt((double)L));
